@@ -64,7 +64,8 @@ typedef enum {
   KVQ_ERR_CUDA = 5,         /* a CUDA runtime call failed (launch, attribute query) */
   KVQ_ERR_DEVICE = 6,       /* a kernel recorded an internal inconsistency */
   KVQ_ERR_TIMEOUT = 7,      /* a bounded wait inside a kernel ran out */
-  KVQ_ERR_UNSUPPORTED = 8   /* valid arguments outside what this library implements */
+  KVQ_ERR_UNSUPPORTED = 8,  /* valid arguments outside what this library implements */
+  KVQ_ERR_INDEX = 9         /* a page number or a position outside its range (device-detected) */
 } kvq_status;
 
 typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
@@ -295,6 +296,148 @@ KVQ_API kvq_status kvq_selftest_timeout(const void* Q, kvq_dtype q_dtype, const 
                                         const int32_t* lengths, int32_t H_q, float scale, void* O,
                                         void* workspace, size_t ws_bytes, int32_t splits, int32_t lose_block,
                                         uint32_t wait_ms, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache: sequences of any length in pages of one pool
+ * ------------------------------------------------------------------------
+ * A serving engine gives each sequence pages from a pool as it grows.  The
+ * pool is a kvq_cache whose "sequences" are pages: pages.B pages of
+ * pages.N_cap tokens (the page size P, a multiple of the group, so that no K
+ * group spans two pages), each holding H_kv heads in the layout above.  A
+ * block table, device int32 [S, max_pages], names sequence b's pages: token t
+ * sits in page table[b][t / P] at row t % P.  Entries past a sequence's last
+ * page are never read.  Pages may be shared by sequences (a common prefix);
+ * a page that kvq_paged_append writes must belong to one sequence only.
+ *
+ * K scales run along tokens, so the group that holds a sequence's last tokens
+ * is packed again whenever one arrives.  The rows it needs are kept beside
+ * the pages: k_tail, device float32 [tail_slots, H_kv, g, D], 16-byte
+ * aligned; row r of a slot is the (rotated) key of token g * (len / g) + r of
+ * the sequence that owns the slot, for r < len % g.  kvq_paged_append reads
+ * and keeps it; a sequence that moves to another slot takes its rows along.
+ *
+ * Batches are ragged: the rows of sequence b's new tokens are rows
+ * [cu[b], cu[b + 1]) of the call's row tensors (cu: device int32 [S + 1],
+ * not decreasing, cu[S] <= T); a sequence may have none.  Rows from cu[S] on
+ * are neither read nor written.  max_new (max_q, max_rows) is an upper bound
+ * of the rows a sequence has in this call, known on the host; lengths count
+ * the new tokens.
+ *
+ * Device-detected errors (kvq_check): KVQ_ERR_LENGTH for a sequence with rows
+ * whose length is below its row count or beyond max_pages * P, or for a cu
+ * that is not as stated (rows are then clamped to [0, T) and max_new);
+ * KVQ_ERR_INDEX for a page number outside [0, pages.B) (nothing is written
+ * there; a read takes page 0 instead), a tail slot outside [0, tail_slots)
+ * (nothing of that sequence is appended) or a position at or past n_pos (its
+ * row is not rotated).
+ */
+typedef struct {
+  kvq_cache pages;
+  float* k_tail;
+  int32_t tail_slots;
+} kvq_paged_cache;
+
+/* Rotation of position pairs: feature pairs (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) where interleaved, i < rot_dim / 2, become
+ * (x c - y s, y c + x s) with c = table[pos][i], s = table[pos][rot_dim / 2 + i];
+ * features from rot_dim on stay as they are.  table: device float32
+ * [n_pos, rot_dim], caller-made.  table NULL: no rotation. */
+typedef struct {
+  const float* table;
+  int32_t n_pos, rot_dim, interleaved;
+} kvq_rope;
+
+/*
+ * Append new tokens to a paged cache: rotate each new key by its position in
+ * the sequence (rope may be NULL: keys come as they are to be kept), pack it
+ * with its group, and pack the V rows.
+ *   K, V       device, rows of H_kv * D in in_dtype; row r starts at element
+ *              r * k_stride (v_stride), so views of a fused projection's
+ *              output can be given as they are.  Strides >= H_kv * D.
+ *   lengths    device int32 [S], counting the new tokens.
+ *   slots      device int32 [S], each sequence's tail slot; NULL: slot b.
+ * Each product and each sum of the rotation is rounded to float32 (no fused
+ * multiply-add), so the pages hold exactly the bytes that kvq_pack writes for
+ * the same rotated float32 rows, however a sequence's tokens were divided
+ * over calls.  Sequences of one call must own different slots and pages.
+ * Errors: KVQ_ERR_ARG, KVQ_ERR_ALIGN (K, V, int32 arrays not aligned to their
+ * element size; cache arrays, k_tail not to 16 bytes), KVQ_ERR_UNSUPPORTED
+ * (D > 256, or g * D > 32768), KVQ_ERR_CUDA.
+ */
+KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* cache, const void* K, int64_t k_stride,
+                                    const void* V, int64_t v_stride, kvq_dtype in_dtype,
+                                    const int32_t* block_table, int32_t max_pages, const int32_t* lengths,
+                                    const int32_t* cu_new, const int32_t* slots, int32_t S, int32_t T,
+                                    int32_t max_new, const kvq_rope* rope, void* stream);
+
+/*
+ * Read tokens of a paged cache back as the values their codes stand for,
+ * (code - qmax) * scale in float32 (rounded once more for KVQ_BF16): tokens
+ * [starts[b], starts[b] + cu[b + 1] - cu[b]) of each sequence into rows
+ * [cu[b], cu[b + 1]) of K and V, device [T, H_kv, D] in out_dtype, 16-byte
+ * aligned.  Either may be NULL (not both).  For moving a sequence elsewhere,
+ * checking a cache, or kernels that want dense keys.  The tokens must have
+ * been appended; a token past max_pages * P gives a zero row and
+ * KVQ_ERR_LENGTH.
+ * Errors: KVQ_ERR_ARG, KVQ_ERR_ALIGN, KVQ_ERR_CUDA.
+ */
+KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* block_table,
+                                    int32_t max_pages, const int32_t* starts, const int32_t* cu_rows,
+                                    int32_t S, int32_t T, int32_t max_rows, void* K, void* V,
+                                    kvq_dtype out_dtype, void* stream);
+
+/*
+ * Attention of a ragged batch of query rows over a paged cache: decode (one
+ * row a sequence), drafted tokens, chunks and whole prompts in one call.
+ * Row i of sequence b's n rows is its position lengths[b] - n + i.
+ *   Q, O     device, [T, H_q, D] in q_dtype, 16-byte aligned; query head h
+ *            reads KV head h / (H_q / H_kv).
+ *   lengths  device int32 [S]: keys of each sequence, this call's tokens
+ *            (already appended) among them.
+ *   causal   nonzero: a row reads the keys up to its own position; 0: all
+ *            lengths[b] keys.
+ *   splits   as kvq_attend.
+ * A row without a visible key is zero.  Sums, the softmax's maximum and sum
+ * and the weighted values are float32; O is rounded once.
+ * Errors: as kvq_attend; KVQ_ERR_UNSUPPORTED also for T * H_q >= 2^30.
+ */
+KVQ_API kvq_status kvq_paged_attend(const void* Q, kvq_dtype q_dtype, const kvq_paged_cache* cache,
+                                    const int32_t* block_table, int32_t max_pages, const int32_t* lengths,
+                                    const int32_t* cu_q, int32_t S, int32_t T, int32_t max_q, int32_t H_q,
+                                    float scale, int32_t causal, void* O, void* workspace, size_t ws_bytes,
+                                    int32_t splits, void* stream);
+
+/* Workspace bytes kvq_paged_attend needs for these arguments on the current
+ * device (host).  Returns 0 for invalid arguments. */
+KVQ_API size_t kvq_paged_workspace_size(const kvq_paged_cache* cache, kvq_dtype q_dtype, int32_t S, int32_t T,
+                                        int32_t max_q, int32_t H_q, int32_t splits);
+
+/* Name of the attention kernel kvq_paged_attend would run, for logs and tests. */
+KVQ_API const char* kvq_paged_kernel_name(const kvq_paged_cache* cache, kvq_dtype q_dtype, int32_t max_q,
+                                          int32_t H_q);
+
+/*
+ * RMS norm of each query and key head and the position rotation, in one pass:
+ *   y = x * w / sqrt(mean(x^2) + eps) over the head's D features, then the
+ * rotation of kvq_rope at positions[t], rounded once to the output's dtype.
+ *   Q, K     device, rows of H_q * D and H_kv * D in dtype; row t starts at
+ *            element t * q_stride (k_stride).  K may be NULL (queries only:
+ *            kvq_paged_append rotates keys itself).
+ *   q_weight, k_weight  device [D] in dtype; NULL: that side is not normed.
+ *   positions device int32 [T]; not read without a rotation.
+ *   Q_out, K_out  device, [T, H_q, D] and [T, H_kv, D] dense; may be the
+ *            input itself where that is dense, and must not overlap it
+ *            otherwise.
+ * A position outside [0, n_pos) is recorded (KVQ_ERR_INDEX); its rows are
+ * normed but not rotated.
+ * Errors: KVQ_ERR_ARG, KVQ_ERR_ALIGN (pointers not aligned to their element
+ * size), KVQ_ERR_UNSUPPORTED (D > 1024), KVQ_ERR_CUDA.
+ */
+KVQ_API kvq_status kvq_qk_norm_rope(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                                    kvq_dtype dtype, int32_t T, int32_t H_q, int32_t H_kv, int32_t D,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const int32_t* positions, const kvq_rope* rope, void* Q_out, void* K_out,
+                                    void* stream);
 
 /* Workspace bytes kvq_attend needs for these arguments on the current
  * device (host).  Returns 0 for invalid arguments. */

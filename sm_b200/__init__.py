@@ -14,6 +14,16 @@ is no fallback of any kind.
                                                   # packed tokens, then an unquantized window
     O = sm_b200.decode_step(Q, cache, lengths, K_tail, V_new, scale)
                                                   # append each sequence's new token, then attend
+
+Paged serving: a pool of pages shared by sequences of any length, ragged
+batches (sequence b's rows are rows [cu[b], cu[b + 1]) of the row tensors).
+
+    cache = sm_b200.PagedCache(pages, H_kv, page_size, D, bits=4, group=32, slots=max_seqs)
+    rope = sm_b200.rope_table(n_pos, rot_dim)
+    Q, K = sm_b200.qk_norm_rope(Q, K, positions, rope, q_weight, k_weight)   # norms and rotation, one pass
+    sm_b200.paged_append(K, V, cache, block_table, lengths, cu, max_new)     # rope=rope rotates K on the way
+    O = sm_b200.paged_attend(Q, cache, block_table, lengths, cu, max_new, scale)
+    K, V = sm_b200.paged_gather(cache, block_table, starts, cu, rows, max_rows)   # tokens back as values
 """
 
 from __future__ import annotations
@@ -27,6 +37,8 @@ __all__ = [
     "KVQError", "PackedCache", "pack", "attend", "workspace_size", "check",
     "launch_count", "kernel_name", "cache_sizes", "lib", "LIB_PATH", "attend_noalloc",
     "attend_window", "workspace_size_window", "decode_step",
+    "PagedCache", "rope_table", "qk_norm_rope", "paged_append", "paged_gather", "paged_attend",
+    "paged_workspace_size", "paged_kernel_name",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkvq.so")
@@ -35,7 +47,7 @@ KVQ_F32, KVQ_BF16 = 0, 1
 STATUS = {
     0: "KVQ_OK", 1: "KVQ_ERR_ARG", 2: "KVQ_ERR_LENGTH", 3: "KVQ_ERR_ALIGN",
     4: "KVQ_ERR_WORKSPACE", 5: "KVQ_ERR_CUDA", 6: "KVQ_ERR_DEVICE", 7: "KVQ_ERR_TIMEOUT",
-    8: "KVQ_ERR_UNSUPPORTED",
+    8: "KVQ_ERR_UNSUPPORTED", 9: "KVQ_ERR_INDEX",
 }
 
 
@@ -54,6 +66,15 @@ class _Cache(ctypes.Structure):
         ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
         ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
     ]
+
+
+class _Paged(ctypes.Structure):
+    _fields_ = [("pages", _Cache), ("k_tail", ctypes.c_void_p), ("tail_slots", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -99,6 +120,21 @@ def _load() -> ctypes.CDLL:
     L.kvq_selftest_timeout.argtypes = [vp, ctypes.c_int, ctypes.POINTER(_Cache), vp, i32, ctypes.c_float, vp, vp,
                                        sz, i32, i32, ctypes.c_uint32, vp]
     L.kvq_selftest_timeout.restype = ctypes.c_int
+    i64, pp, rp = ctypes.c_int64, ctypes.POINTER(_Paged), ctypes.POINTER(_Rope)
+    L.kvq_paged_append.argtypes = [pp, vp, i64, vp, i64, ctypes.c_int, vp, i32, vp, vp, vp, i32, i32, i32, rp, vp]
+    L.kvq_paged_append.restype = ctypes.c_int
+    L.kvq_paged_gather.argtypes = [pp, vp, i32, vp, vp, i32, i32, i32, vp, vp, ctypes.c_int, vp]
+    L.kvq_paged_gather.restype = ctypes.c_int
+    L.kvq_paged_attend.argtypes = [vp, ctypes.c_int, pp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float, i32, vp,
+                                   vp, sz, i32, vp]
+    L.kvq_paged_attend.restype = ctypes.c_int
+    L.kvq_paged_workspace_size.argtypes = [pp, ctypes.c_int, i32, i32, i32, i32, i32]
+    L.kvq_paged_workspace_size.restype = sz
+    L.kvq_paged_kernel_name.argtypes = [pp, ctypes.c_int, i32, i32]
+    L.kvq_paged_kernel_name.restype = ctypes.c_char_p
+    L.kvq_qk_norm_rope.argtypes = [vp, i64, vp, i64, ctypes.c_int, i32, i32, i32, i32, vp, vp, ctypes.c_float, vp, rp,
+                                   vp, vp, vp]
+    L.kvq_qk_norm_rope.restype = ctypes.c_int
     return L
 
 
@@ -370,6 +406,273 @@ def attend_window(Q: torch.Tensor, cache: PackedCache, lengths: torch.Tensor, K_
                               W_cap, H_q, Lq, float(scale), out.data_ptr(), workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), int(splits),
                               _stream(cache.device)), "kvq_attend_window")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# paged cache
+# ---------------------------------------------------------------------------
+class PagedCache:
+    """A pool of ``pages`` pages of ``page_size`` tokens (a multiple of the
+    group) and the float32 rows of each sequence's unfinished K group.
+
+    The four arrays are laid out as a PackedCache of ``pages`` sequences with
+    capacity ``page_size`` (``include/kvq.h``); ``k_tail`` is float32
+    [slots, H_kv, group, D].  ``buffers`` (k_codes, k_scales, v_codes,
+    v_scales, k_tail) makes the cache over memory the caller owns.  The buffers
+    must not be rebound: the C struct the calls pass is built once."""
+
+    def __init__(self, pages: int, H_kv: int, page_size: int, D: int, bits: int = 4, group: int = 32,
+                 slots: int = 1, device="cuda", buffers=None):
+        self.pages, self.H_kv, self.page_size, self.D = int(pages), int(H_kv), int(page_size), int(D)
+        self.bits, self.group, self.slots = int(bits), int(group), int(slots)
+        sizes = cache_sizes(pages, H_kv, page_size, D, bits, group)
+        if self.page_size % self.group:
+            raise ValueError("page_size must be a multiple of group")
+        if self.slots < 1:
+            raise ValueError("slots must be at least 1")
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        tail = self.slots * self.H_kv * self.group * self.D
+        want = tuple(zip(("k_codes", "k_scales", "v_codes", "v_scales", "k_tail"),
+                         (torch.uint8, torch.float32, torch.uint8, torch.float32, torch.float32),
+                         (sizes[0], sizes[1] // 4, sizes[2], sizes[3] // 4, tail)))
+        if buffers is None:
+            buffers = [torch.zeros(n, dtype=dt, device=dev) for _, dt, n in want]
+        if len(buffers) != len(want):
+            raise ValueError("buffers must be (k_codes, k_scales, v_codes, v_scales, k_tail)")
+        for t, (name, dt, n) in zip(buffers, want):
+            _check_cuda(t, name, dev)
+            if t.dtype != dt or t.numel() != n:
+                raise ValueError(f"{name} must hold {n} elements of {dt}")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, k_tail = buffers
+        self.k_tail = k_tail.view(self.slots, self.H_kv, self.group, self.D)
+        self.device = dev
+        self._struct = _Paged(_Cache(self.bits, self.group, self.pages, self.H_kv, self.page_size, self.D,
+                                     self.k_codes.data_ptr(), self.k_scales.data_ptr(),
+                                     self.v_codes.data_ptr(), self.v_scales.data_ptr()),
+                              self.k_tail.data_ptr(), self.slots)
+        self._ref = ctypes.byref(self._struct)
+        self._ws = {}                      # (dtype, S, T, max_q, H_q, splits) -> workspace bytes
+
+    def struct(self) -> _Paged:
+        return self._struct
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size()
+                   for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.k_tail))
+
+
+def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The float32 [n_pos, rot_dim] table of kvq_rope: cos of pos * base^(-2 i
+    / rot_dim) for the rot_dim / 2 pairs, then sin; the angles are formed in
+    float64, so far positions keep their phase."""
+    if n_pos < 1 or rot_dim < 2 or rot_dim % 2:
+        raise ValueError("n_pos must be positive and rot_dim positive and even")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * float(base) ** (-i / rot_dim)
+    return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
+
+
+def _call(dev: torch.device, fn, name: str, *args) -> None:
+    """fn(*args, current stream of dev) with dev current."""
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise KVQError(st, name)
+
+
+def _rope_arg(rope: torch.Tensor | None, interleaved: bool, D: int, dev: torch.device):
+    if rope is None:
+        return None
+    _check_cuda(rope, "rope", dev)
+    if rope.dtype != torch.float32 or rope.dim() != 2:
+        raise ValueError("rope must be float32 [n_pos, rot_dim]")
+    n_pos, rot = rope.shape
+    if rot < 2 or rot % 2 or rot > D or n_pos < 1:
+        raise ValueError("rot_dim must be even, at least 2 and at most D")
+    return _Rope(rope.data_ptr(), n_pos, rot, int(bool(interleaved)))
+
+
+def _check_rows(t: torch.Tensor, name: str, T: int, heads: int, D: int, dev: torch.device) -> int:
+    """The row stride of t [T, heads, D], whose rows may lie any distance apart."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if t.dim() != 3 or tuple(t.shape) != (T, heads, D):
+        raise ValueError(f"{name} must be [{T}, {heads}, {D}]")
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name}: the heads of a row must lie one after the other")
+    if T > 1 and st[0] < heads * D:
+        raise ValueError(f"{name}: rows must not overlap")
+    return st[0] if T > 1 else heads * D
+
+
+def _check_index(t: torch.Tensor, name: str, n: int, dev: torch.device) -> None:
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n:
+        raise ValueError(f"{name} must be int32 [{n}]")
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous on {dev}")
+
+
+def _check_batch(cache: PagedCache, block_table: torch.Tensor, lengths: torch.Tensor, cu: torch.Tensor,
+                 name: str = "lengths") -> int:
+    """Number of sequences of a ragged call."""
+    dev = cache.device
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [S, max_pages]")
+    if block_table.device != dev or not block_table.is_contiguous():
+        raise ValueError(f"block_table must be contiguous on {dev}")
+    S = block_table.shape[0]
+    _check_index(lengths, name, S, dev)
+    _check_index(cu, "cu", S + 1, dev)
+    return S
+
+
+def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor | None,
+                 rope: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """RMS norm of each head (a side without a weight is not normed) and the
+    rotation at ``positions`` (int32 [T]; rope None: none), one pass.  Q
+    [T, H_q, D], K [T, H_kv, D] or None, fp32/bf16, rows any distance apart
+    (views of a fused projection); returns dense (Q', K')."""
+    dev = Q.device
+    if not Q.is_cuda:
+        raise ValueError("Q must be on a CUDA device")
+    if Q.dim() != 3:
+        raise ValueError("Q must be [T, H_q, D]")
+    T, H_q, D = Q.shape
+    code = _dtype_code(Q)
+    qs = _check_rows(Q, "Q", T, H_q, D, dev)
+    H_kv, ks = 0, 0
+    if K is not None:
+        if K.dim() != 3 or K.dtype != Q.dtype:
+            raise ValueError("K must be [T, H_kv, D] of Q's dtype")
+        H_kv = K.shape[1]
+        ks = _check_rows(K, "K", T, H_kv, D, dev)
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.device != dev or w.dtype != Q.dtype or w.dim() != 1 or w.numel() != D
+                              or not w.is_contiguous()):
+            raise ValueError(f"{n} must be contiguous [D] of Q's dtype on {dev}")
+    r = _rope_arg(rope, interleaved, D, dev)
+    if r is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _check_index(positions, "positions", T, dev)
+    if q_out is None:
+        q_out = torch.empty((T, H_q, D), dtype=Q.dtype, device=dev)
+    if k_out is None and K is not None:
+        k_out = torch.empty((T, H_kv, D), dtype=Q.dtype, device=dev)
+    for o, x, n in ((q_out, Q, "q_out"), (k_out, K, "k_out")):
+        if x is not None and (o.shape != x.shape or o.dtype != x.dtype or o.device != dev or not o.is_contiguous()):
+            raise ValueError(f"{n} must be contiguous and match its input")
+    if T == 0:
+        return q_out, k_out
+    _call(dev, lib.kvq_qk_norm_rope, "kvq_qk_norm_rope", Q.data_ptr(), qs, K.data_ptr() if K is not None else None, ks,
+          code, T, H_q, H_kv, D, q_weight.data_ptr() if q_weight is not None else None,
+          k_weight.data_ptr() if k_weight is not None else None, float(eps),
+          positions.data_ptr() if r is not None else None, ctypes.byref(r) if r is not None else None,
+          q_out.data_ptr(), k_out.data_ptr() if K is not None else None)
+    return q_out, k_out
+
+
+def paged_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
+                 lengths: torch.Tensor, cu: torch.Tensor, max_new: int, rope: torch.Tensor | None = None,
+                 interleaved: bool = False, slots: torch.Tensor | None = None) -> None:
+    """Append the ragged rows K, V [T, H_kv, D] (rows any distance apart) to
+    the sequences' pages: sequence b's rows [cu[b], cu[b + 1]) become its
+    tokens lengths[b] - n .. lengths[b] - 1 (lengths count them), K rotated by
+    its position on the way if ``rope`` is given.  ``slots`` int32 [S]: each
+    sequence's row of ``cache.k_tail`` (default: b)."""
+    dev, H, D = cache.device, cache.H_kv, cache.D
+    S = _check_batch(cache, block_table, lengths, cu)
+    if K.dim() != 3 or K.dtype != V.dtype:
+        raise ValueError("K and V must be [T, H_kv, D] of one dtype")
+    T = K.shape[0]
+    ks, vs = _check_rows(K, "K", T, H, D, dev), _check_rows(V, "V", T, H, D, dev)
+    if slots is not None:
+        _check_index(slots, "slots", S, dev)
+    elif S > cache.slots:
+        raise ValueError("more sequences than the cache has tail slots")
+    r = _rope_arg(rope, interleaved, D, dev)
+    if T == 0 or S == 0:
+        return
+    _call(dev, lib.kvq_paged_append, "kvq_paged_append", cache._ref, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(K),
+          block_table.data_ptr(), block_table.shape[1], lengths.data_ptr(), cu.data_ptr(),
+          slots.data_ptr() if slots is not None else None, S, T, int(max_new),
+          ctypes.byref(r) if r is not None else None)
+
+
+def paged_gather(cache: PagedCache, block_table: torch.Tensor, starts: torch.Tensor, cu: torch.Tensor, rows: int,
+                 max_rows: int, dtype: torch.dtype = torch.float32):
+    """Tokens [starts[b], starts[b] + cu[b + 1] - cu[b]) of each sequence as
+    the values their codes stand for: dense K, V [rows, H_kv, D], rows
+    [cu[b], cu[b + 1]) of them (others are left unwritten)."""
+    dev = cache.device
+    S = _check_batch(cache, block_table, starts, cu, "starts")
+    K = torch.empty((rows, cache.H_kv, cache.D), dtype=dtype, device=dev)
+    V = torch.empty_like(K)
+    code = _dtype_code(K)
+    if rows > 0 and S > 0:
+        _call(dev, lib.kvq_paged_gather, "kvq_paged_gather", cache._ref, block_table.data_ptr(), block_table.shape[1],
+              starts.data_ptr(), cu.data_ptr(), S, rows, int(max_rows), K.data_ptr(), V.data_ptr(), code)
+    return K, V
+
+
+def paged_workspace_size(cache: PagedCache, dtype: torch.dtype, S: int, T: int, max_q: int, H_q: int,
+                         splits: int = 0) -> int:
+    key = (dtype, S, T, max_q, H_q, splits)
+    n = cache._ws.get(key)
+    if n is None:
+        n = int(lib.kvq_paged_workspace_size(cache._ref, KVQ_F32 if dtype == torch.float32 else KVQ_BF16, S, T, max_q,
+                                             H_q, splits))
+        if len(cache._ws) > 4096:          # ragged batches: T changes from call to call
+            cache._ws.clear()
+        cache._ws[key] = n
+    return n
+
+
+def paged_kernel_name(cache: PagedCache, dtype: torch.dtype, max_q: int, H_q: int) -> str:
+    return lib.kvq_paged_kernel_name(cache._ref, KVQ_F32 if dtype == torch.float32 else KVQ_BF16, int(max_q),
+                                     int(H_q)).decode()
+
+
+def paged_attend(Q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, lengths: torch.Tensor,
+                 cu: torch.Tensor, max_q: int, scale: float, causal: bool = True, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, splits: int = 0) -> torch.Tensor:
+    """Attention of the ragged query rows Q [T, H_q, D] over the sequences'
+    pages: row i of sequence b's n rows is position lengths[b] - n + i; causal:
+    it reads the keys up to its own position, else all lengths[b] keys.
+    ``max_q``: upper bound of the rows a sequence has.  Returns O like Q; rows
+    from cu[S] on are left as they were."""
+    dev = cache.device
+    S = _check_batch(cache, block_table, lengths, cu)
+    _check_cuda(Q, "Q", dev)
+    if Q.dim() != 3 or Q.shape[2] != cache.D:
+        raise ValueError("Q must be [T, H_q, D]")
+    T, H_q, _ = Q.shape
+    code = _dtype_code(Q)
+    if out is None:
+        out = torch.empty_like(Q)
+    else:
+        _check_cuda(out, "out", dev)
+        if out.shape != Q.shape or out.dtype != Q.dtype:
+            raise ValueError("out must match Q")
+    if T == 0 or S == 0:
+        return out
+    need = paged_workspace_size(cache, Q.dtype, S, T, int(max_q), H_q, int(splits))
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    else:
+        _check_cuda(workspace, "workspace", dev)
+    _call(dev, lib.kvq_paged_attend, "kvq_paged_attend", Q.data_ptr(), code, cache._ref, block_table.data_ptr(),
+          block_table.shape[1], lengths.data_ptr(), cu.data_ptr(), S, T, int(max_q), H_q, float(scale), int(bool(causal)),
+          out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(splits))
     return out
 
 
