@@ -262,6 +262,7 @@ struct AttendImpl {
   kvq_status (*launch)(const AttendArgs&, cudaStream_t);
 };
 const AttendImpl& generic_impl();
+const AttendImpl& rows_impl();       // few rows a KV head
 
 }  // namespace paged
 }  // namespace kvq
