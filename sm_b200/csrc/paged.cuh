@@ -241,8 +241,9 @@ __device__ __forceinline__ Item plan_item(const PlanView& v, int i) {
 // ---------------------------------------------------------------------------
 // merge of partial states
 // ---------------------------------------------------------------------------
-// partials: [2 * workers slots][RI][D + 2] (m in log2 units, z, u), or
-// feature-major [slots][RI / 32][D + 2][32].
+// partials: [2 * workers slots][RI * D + RI * 2] (u rows, then (m, z) per row;
+// m in log2 units), or feature-major [slots][8][D + 2][32]: fields m, z, u of
+// 32 rows each, tile t's rows from 128 t on.
 struct MergeCall {
   Batch t;
   PlanMem plan;
@@ -251,7 +252,7 @@ struct MergeCall {
   const float* partials;
   void* O;
   int o_dtype;
-  int tile_rows;                 // feature-major: rows per 128-lane tile (0: row-major)
+  int tile_rows;                 // feature-major: rows of a tile (0: row-major)
 };
 kvq_status launch_merge(const MergeCall& c, cudaStream_t s);
 
@@ -263,6 +264,7 @@ struct AttendImpl {
 };
 const AttendImpl& generic_impl();
 const AttendImpl& rows_impl();       // few rows a KV head
+const AttendImpl& chunk_impl();      // many rows a KV head
 
 }  // namespace paged
 }  // namespace kvq

@@ -29,7 +29,10 @@ kvq_status check_pool(const kvq_paged_cache* c, const int32_t* table, int32_t ma
   return KVQ_OK;
 }
 
-const AttendImpl& choose(const AttendArgs& a) { return rows_impl().applies(a) ? rows_impl() : generic_impl(); }
+const AttendImpl& choose(const AttendArgs& a) {
+  if (chunk_impl().applies(a)) return chunk_impl();
+  return rows_impl().applies(a) ? rows_impl() : generic_impl();
+}
 
 bool fill_sizes(const kvq_paged_cache* c, kvq_dtype q_dtype, int32_t S, int32_t T, int32_t max_q, int32_t H_q,
                 int32_t splits, AttendArgs* a) {

@@ -1,0 +1,756 @@
+// Paged attention of many query rows a KV head (chunks, prompts, drafts of
+// wide groups) on the tcgen05 tensor cores: D 64 or 128, groups of 32, 4- or
+// 8-bit codes, bf16 rows.
+//
+// An item (paged.cuh) is up to two tiles of 128 query rows of one sequence,
+// token-major with the KV head's G query heads side by side: a tile holds
+// floor(128 / G) tokens, fetched by one 4-D TMA copy per 64 features (feature,
+// head of the group, KV head, token).  Per block of 128 keys the packed bytes
+// come page by page, are decoded -- (code - qmax) * scale, rounded once to
+// bf16 -- into shared-memory tiles, S = Q K^T goes to tensor memory (TMEM),
+// the softmax turns S into P (bf16) in place and O += P V accumulates in TMEM.
+// At 128 rows a block costs 4 * 128 * D * 128 FLOPs for 160 (288) bytes a key
+// at D = 128: the tensor pipe bounds it, not memory.  Two row tiles are in
+// flight so that the tensor cores work on one while the other is in the
+// softmax.
+//
+// Causal rows: a column past a row's position takes no part in its maximum and
+// its p is zero.  A *value* that is not finite would still reach such a row
+// through 0 * inf, so its token's scale is taken as zero in the tile and the
+// token is remembered: rows that do see it become NaN at the segment's end.
+//
+// The softmax's reference maximum is lazy: it moves, and O and z are rescaled,
+// only when a block's maximum outruns it by more than 8 in log2 units.  Any
+// reference that never falls more than that below the running maximum gives
+// the same u / z in exact arithmetic.
+//
+// Warp roles (20 warps, 96 registers each):
+//   0        producer: lanes 0..3 copy 32 keys each (codes and scales) of a K
+//            or V unit into a ring; order K(0), K(1), V(0), K(2), V(1), ...
+//   1        MMA issuer (one thread) and TMEM owner
+//   2        Q loader
+//   4..7     softmax of tile 0 (a thread a row), 8..11 of tile 1
+//   12..19   decode: warp w converts 16 keys of each unit
+//   3        idle
+// TMEM columns: S/P of tile t at [128 t, +128), O at [256 + 128 t, +D).
+// Shared-memory tiles use the 128-byte-swizzled UMMA layout of tc_common.cuh.
+#include <cuda.h>
+
+#include "f32x2.cuh"
+#include "paged.cuh"
+#include "tc_common.cuh"
+
+namespace kvq {
+namespace paged {
+namespace {
+
+using namespace tc;
+
+constexpr int kBT = 128;
+constexpr int kThreads = 640;
+constexpr int kDecodeWarps = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.f;
+constexpr int kTileHalf = kBT * 128;              // 16 KB: 128 rows x 64 bf16
+constexpr int kMaxUnits = 6;
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = D / 64 * kTileHalf;
+  static constexpr int kQ = 0;                     // two row tiles
+  static constexpr int kK = 2 * kTile;             // two K tiles
+  static constexpr int kV = kK + 2 * kTile;        // one V tile
+  static constexpr int kRing = kV + kTile;
+  static constexpr int kRingBytes = 54 * 1024;
+  static constexpr int kBar = kRing + kRingBytes;
+  static constexpr int kMisc = kBar + 32 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kPre = kMisc + 80;          // int pre[S + 1] (inline plan)
+};
+
+enum Bar {
+  RING_FULL = 0,                 // [kMaxUnits]
+  RING_EMPTY = 6,                // [kMaxUnits]
+  K_READY = 12,                  // [2]
+  K_FREE = 14,                   // [2]
+  V_READY = 16,
+  V_FREE = 17,
+  Q_READY = 18,
+  Q_FREE = 19,
+  S_FULL = 20,                   // [2]
+  P_FULL = 22,                   // [2]
+  PV_DONE = 24,                  // [2]
+};
+
+struct Params {
+  Batch t;
+  PlanMem plan;
+  const uint8_t* k_codes;
+  const float* k_scales;
+  const uint8_t* v_codes;
+  const float* v_scales;
+  float qscale;                  // scale * log2(e)
+  __nv_bfloat16* O;
+  float* partials;               // [2 ctas][8][D + 2][32]
+  int ctas, RI, TT;              // rows of an item, tokens of a row tile
+  unsigned int* err;
+};
+
+// ---------------------------------------------------------------------------
+// a CTA's blocks
+// ---------------------------------------------------------------------------
+struct Place {
+  int i, h, j, nb;
+  long long left;
+  Item it;
+  SeqView s;
+  bool start;                    // first block of a segment
+};
+struct Walk {
+  const Params& p;
+  PlanView v;
+  __device__ __forceinline__ void enter(Place& a) const {
+    a.it = plan_item(v, a.i);
+    a.s = seq_view(p.t, a.it.b);
+    a.nb = v.pre[a.i + 1] - v.pre[a.i];
+  }
+  __device__ __forceinline__ Place begin(const Range& r) const {
+    Place a;
+    a.left = r.g1 - r.g0;
+    a.start = true;
+    if (a.left <= 0) return a;
+    a.i = find_item(v, p.t.H, r.g0);
+    enter(a);
+    const long long off = r.g0 - static_cast<long long>(p.t.H) * v.pre[a.i];
+    a.h = static_cast<int>(off / a.nb);
+    a.j = static_cast<int>(off % a.nb);
+    return a;
+  }
+  __device__ __forceinline__ void next(Place& a) const {
+    if (--a.left <= 0) return;
+    a.start = false;
+    if (++a.j < a.nb) return;
+    a.start = true;
+    a.j = 0;
+    if (++a.h == p.t.H) {
+      a.h = 0;
+      do ++a.i;
+      while (v.pre[a.i + 1] == v.pre[a.i]);
+      enter(a);
+    }
+  }
+  // last block of a segment
+  __device__ __forceinline__ bool last(const Place& a) const { return a.left == 1 || a.j + 1 == a.nb; }
+  // row tiles of the place's item
+  __device__ __forceinline__ int tiles(const Place& a) const {
+    return a.s.n * p.t.G - a.it.r0 > p.TT * p.t.G && p.RI > p.TT * p.t.G ? 2 : 1;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// decode of a unit's 16 keys to bf16 values in a swizzled tile
+// ---------------------------------------------------------------------------
+// A lane takes 16 features (two 16-byte chunks of the tile) of a token; at D =
+// 128 a quarter warp is one token, and lanes q and q + 4 store their chunks in
+// opposite order, so the quarter warp meets eight bank groups; at D = 64 it is
+// two tokens, whose rows swizzle differently.
+template <int BITS, int D, bool kV>
+__device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned char* dst, int wk, int lane, int nv,
+                                            int t_base, unsigned long long seg_key, unsigned long long* s_bad) {
+  constexpr int kCb = D * BITS / 8, QN = D / 16, TPP = 32 / QN;
+  const int q = lane % QN, tt = lane / QN;
+  const bool swap = D == 128 && (q & 4) != 0;
+  const float* sc = reinterpret_cast<const float*>(u + kBT * kCb);
+  u64 ks[8];                                       // slot 4 i + r: pair r of 8-feature half i ^ swap
+  if (!kV) {
+    if (16 * wk < nv) {
+      const float4* s4 = reinterpret_cast<const float4*>(sc + (wk >> 1) * D + 16 * q);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ci = i ^ (swap ? 1 : 0);
+        const float4 v0 = s4[2 * ci], v1 = s4[2 * ci + 1];
+        ks[4 * i] = pack2(v0.x, v0.y);
+        ks[4 * i + 1] = pack2(v0.z, v0.w);
+        ks[4 * i + 2] = pack2(v1.x, v1.y);
+        ks[4 * i + 3] = pack2(v1.z, v1.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ks[i] = 0ull;
+    }
+  }
+  const u64 mul = pack2(256.f, 16.f), add = pack2(-263.f, -23.f), sub = pack2(-8388735.f, -8388735.f);
+#pragma unroll 1
+  for (int it = 0; it < 16 / TPP; ++it) {
+    const int t = 16 * wk + TPP * it + tt;
+    uint4 o[2];
+    if (t < nv) {
+      u64 s2 = 0ull;
+      if (kV) {
+        float s = sc[D / 32 * t + (q >> 1)];
+        if (!(fabsf(s) < INFINITY)) {              // remembered: rows that see the token become NaN
+          atomicMax(s_bad, seg_key | static_cast<unsigned>(0x7fffffff - (t_base + t)));
+          s = 0.f;
+        }
+        s2 = pack2(s, s);
+      }
+      uint32_t h[8];
+      if (BITS == 4) {
+        const uint2 w2 = *reinterpret_cast<const uint2*>(u + t * kCb + 8 * q);
+        const uint32_t w[2] = {swap ? w2.y : w2.x, swap ? w2.x : w2.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const u64 f = fma2(nibble_pair(byte_at15(w[i], r)), mul, add);
+            const u64 x = mul2(f, kV ? s2 : ks[4 * i + r]);
+            h[4 * i + r] = pack_bf16(lo_f(x), hi_f(x));
+          }
+      } else {
+        const uint4 w4 = *reinterpret_cast<const uint4*>(u + t * kCb + 16 * q);
+        const uint32_t w[4] = {swap ? w4.z : w4.x, swap ? w4.w : w4.y, swap ? w4.x : w4.z, swap ? w4.y : w4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const u64 f = add2(byte_pair(w[i], r), sub);
+            const u64 x = mul2(f, kV ? s2 : ks[2 * i + r / 2]);
+            h[2 * i + r / 2] = pack_bf16(lo_f(x), hi_f(x));
+          }
+      }
+      o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    } else {
+      o[0] = make_uint4(0u, 0u, 0u, 0u);
+      o[1] = o[0];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int ch = 2 * q + (i ^ (swap ? 1 : 0));
+      *reinterpret_cast<uint4*>(dst + (ch >> 3) * kTileHalf + swz(t, ch & 7)) = o[i];
+    }
+  }
+}
+
+// Maximum (kMin: minimum) of 64 raw scores held in registers.
+template <bool kMin>
+__device__ __forceinline__ float row_extreme(const uint32_t (&sr)[64]) {
+  auto f = [](uint32_t x) { return __uint_as_float(x); };
+  auto op3 = [](float a, float b, float c) { return kMin ? min3(a, b, c) : max3(a, b, c); };
+  float acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    acc[j] = op3(f(sr[j]), f(sr[8 + j]), f(sr[16 + j]));
+    acc[j] = op3(acc[j], f(sr[24 + j]), f(sr[32 + j]));
+    acc[j] = op3(acc[j], f(sr[40 + j]), f(sr[48 + j]));
+  }
+  const float a = op3(acc[0], acc[1], acc[2]);
+  const float b = op3(acc[3], acc[4], acc[5]);
+  const float c = op3(acc[6], acc[7], a);
+  float r = op3(b, c, f(sr[56]));
+#pragma unroll
+  for (int j = 57; j < 63; j += 2) r = op3(r, f(sr[j]), f(sr[j + 1]));
+  return op3(r, f(sr[63]), f(sr[63]));
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ CUtensorMap qmap, Params p) {
+  using M = Smem<D>;
+  griddep_wait();
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw_addr = su(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  unsigned char* sm = smem_raw + (base - raw_addr);
+  int* s_pre = reinterpret_cast<int*>(sm + M::kPre);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + M::kMisc + 4);
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + M::kMisc + 8);
+  const uint32_t bar0 = base + M::kBar;
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int H = p.t.H, G = p.t.G, TR = p.TT * G;
+  constexpr int cb = D * BITS / 8;
+  constexpr int kScales = D * 16;                         // scale bytes of a unit (K: 4 groups x D; V: 128 x D / 32)
+  constexpr int unit_bytes = kBT * cb + kScales;
+  constexpr uint32_t nu = M::kRingBytes / unit_bytes < kMaxUnits ? M::kRingBytes / unit_bytes : kMaxUnits;
+
+  if (!p.plan.count && warp == 0) warp_prefix(p.t, p.RI, kBT, s_pre);
+  if (threadIdx.x == 32) {
+    *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) s_bad[i] = 0;
+    for (uint32_t u = 0; u < nu; ++u) {
+      mbar_init(bar(RING_FULL + u), 1);
+      mbar_init(bar(RING_EMPTY + u), kDecodeWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(K_READY + i), kDecodeWarps);
+      mbar_init(bar(K_FREE + i), 1);
+      mbar_init(bar(S_FULL + i), 1);
+      mbar_init(bar(P_FULL + i), 4);
+      mbar_init(bar(PV_DONE + i), 1);
+    }
+    mbar_init(bar(V_READY), kDecodeWarps);
+    mbar_init(bar(V_FREE), 1);
+    mbar_init(bar(Q_READY), 1);
+    mbar_init(bar(Q_FREE), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + M::kMisc),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + M::kMisc);
+
+  const Walk walk{p, plan_view(p.plan, s_pre, p.t.S)};
+  const Range wr = worker_range(walk.v, H, p.ctas, blockIdx.x);
+  if (wr.g0 < wr.g1) {
+    if (warp == 0) {
+      // ======================= producer =======================
+      Place kc = walk.begin(wr), vc = kc;
+      uint32_t n = 0;
+      auto unit = [&](const Place& c, bool is_v) {
+        const uint32_t slot = n % nu;
+        const int t0 = c.j * kBT;
+        const int nv = min(kBT, c.s.len - t0);
+        const int pieces = (nv + 31) / 32;                // whole 32-key groups: a page holds them all
+        const uint32_t dst = base + M::kRing + slot * unit_bytes;
+        const uint32_t fb = bar(RING_FULL + slot);
+        int page = 0, at = 0;
+        if (lane < pieces) {
+          const int t = t0 + 32 * lane;
+          page = read_page(__ldg(p.t.table + static_cast<long long>(c.it.b) * p.t.max_pages + t / p.t.P), p.t.pages,
+                           p.err);
+          at = t % p.t.P;
+        }
+        if (lane == 0) {
+          if (n >= nu) wait_bar(bar(RING_EMPTY + slot), ((n / nu) - 1) & 1u, p.err, abort_flag);
+          mbar_expect_tx(fb, static_cast<uint32_t>(pieces * (32 * cb + kScales / 4)));
+        }
+        __syncwarp();
+        if (lane < pieces) {
+          const long long tok = (static_cast<long long>(page) * H + c.h) * p.t.P + at;
+          const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + tok * cb;
+          const float* scales = is_v ? p.v_scales + tok * (D / 32) : p.k_scales + tok / 32 * D;
+          bulk_g2s(dst + lane * 32 * cb, codes, 32 * cb, fb);
+          bulk_g2s(dst + kBT * cb + lane * (kScales / 4), scales, kScales / 4, fb);
+        }
+        __syncwarp();
+        ++n;
+      };
+      unit(kc, false);
+      walk.next(kc);
+      while (vc.left > 0) {
+        if (kc.left > 0) {
+          unit(kc, false);
+          walk.next(kc);
+        }
+        unit(vc, true);
+        walk.next(vc);
+      }
+    } else if (warp == 1) {
+      // ======================= MMA issuer =======================
+      if (lane == 0) {
+        const uint32_t idesc_qk = instr_desc(kBT, false);
+        const uint32_t idesc_pv = instr_desc(D, true);
+        auto qk = [&](int t, uint32_t k) {
+          const uint32_t kt = base + M::kK + (k & 1u) * M::kTile;
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t q_addr = base + M::kQ + t * M::kTile + (i >> 2) * kTileHalf + (i & 3) * 32;
+            const uint32_t k_addr = kt + (i >> 2) * kTileHalf + (i & 3) * 32;
+            mma_ss(tmem + 128u * t, smem_desc(q_addr, 16, 1024), smem_desc(k_addr, 16, 1024), idesc_qk, i > 0);
+          }
+          mma_commit(bar(S_FULL + t));
+        };
+        uint32_t done[2] = {0, 0};                          // P V products issued per tile
+        auto pv = [&](int t, bool first) {
+          wait_bar(bar(P_FULL + t), done[t] & 1u, p.err, abort_flag);
+          tc_fence_after();
+          for (int i = 0; i < kBT / 16; ++i) {
+            const uint32_t v_addr = base + M::kV + i * 16 * 128;
+            mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * i, smem_desc(v_addr, kTileHalf, 1024), idesc_pv,
+                   (!first) || (i > 0));
+          }
+          mma_commit(bar(PV_DONE + t));
+          ++done[t];
+        };
+        // S of a tile overwrites its P: the last P V product must be done
+        auto pv_done = [&](int t) {
+          if (done[t] > 0) {
+            wait_bar(bar(PV_DONE + t), (done[t] - 1) & 1u, p.err, abort_flag);
+            tc_fence_after();
+          }
+        };
+        Place c = walk.begin(wr), cn = c;
+        uint32_t sq = 0;
+        wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
+        ++sq;
+        wait_bar(bar(K_READY), 0u, p.err, abort_flag);
+        tc_fence_after();
+        for (int t = 0; t < walk.tiles(c); ++t) qk(t, 0);
+        mma_commit(bar(K_FREE));
+        if (walk.last(c)) mma_commit(bar(Q_FREE));
+        walk.next(cn);
+        for (uint32_t k = 0; c.left > 0; ++k) {
+          const bool more = cn.left > 0, boundary = more && cn.start;
+          const bool two = walk.tiles(c) == 2;
+          wait_bar(bar(V_READY), k & 1u, p.err, abort_flag);
+          tc_fence_after();
+          pv(0, c.start);
+          if (more && !boundary) {
+            wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
+            pv_done(0);
+            tc_fence_after();
+            qk(0, k + 1);
+          }
+          if (two) pv(1, c.start);
+          mma_commit(bar(V_FREE));
+          if (more) {
+            if (boundary) {
+              wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
+              ++sq;
+              wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
+              pv_done(0);
+              tc_fence_after();
+              qk(0, k + 1);
+            }
+            if (walk.tiles(cn) == 2) {
+              pv_done(1);
+              tc_fence_after();
+              qk(1, k + 1);
+            }
+            mma_commit(bar(K_FREE + ((k + 1) & 1u)));
+            if (walk.last(cn)) mma_commit(bar(Q_FREE));
+          }
+          c = cn;
+          walk.next(cn);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ======================= Q loader =======================
+      if (lane == 0) {
+        uint32_t s = 0;
+        for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
+          if (!c.start) continue;
+          if (s > 0) wait_bar(bar(Q_FREE), (s - 1) & 1u, p.err, abort_flag);
+          ++s;
+          const int nt = walk.tiles(c), tok = c.s.q0 + c.it.r0 / G;
+          mbar_expect_tx(bar(Q_READY), static_cast<uint32_t>(nt * (D / 64) * TR * 128));
+          for (int t = 0; t < nt; ++t)
+            for (int half = 0; half < D / 64; ++half)
+              tma_load_4d(base + M::kQ + t * M::kTile + half * kTileHalf, &qmap, 64 * half, 0, c.h, tok + t * p.TT,
+                          bar(Q_READY));
+        }
+      }
+    } else if (warp >= 12) {
+      // ======================= decode =======================
+      const int wk = warp - 12;
+      Place kc = walk.begin(wr), vc = kc;
+      uint32_t n = 0, kb = 0, vb = 0, seg = 0;
+      auto decode = [&](const Place& c, bool is_v) {
+        const uint32_t slot = n % nu;
+        wait_bar(bar(RING_FULL + slot), (n / nu) & 1u, p.err, abort_flag);
+        if (!is_v && kb >= 2) wait_bar(bar(K_FREE + (kb & 1u)), ((kb >> 1) - 1) & 1u, p.err, abort_flag);
+        if (is_v && vb >= 1) wait_bar(bar(V_FREE), (vb - 1) & 1u, p.err, abort_flag);
+        const unsigned char* u = sm + M::kRing + slot * unit_bytes;
+        const int t0 = c.j * kBT, nv = min(kBT, c.s.len - t0);
+        if (is_v) {
+          if (c.start) ++seg;
+          decode_unit<BITS, D, true>(u, sm + M::kV, wk, lane, nv, t0, static_cast<unsigned long long>(seg) << 32,
+                                     s_bad + (seg & 7u));
+        } else {
+          decode_unit<BITS, D, false>(u, sm + M::kK + (kb & 1u) * M::kTile, wk, lane, nv, 0, 0, nullptr);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(is_v ? V_READY : K_READY + (kb & 1u)));
+          mbar_arrive(bar(RING_EMPTY + slot));
+        }
+        ++n;
+        if (is_v) ++vb; else ++kb;
+      };
+      decode(kc, false);
+      walk.next(kc);
+      while (vc.left > 0) {
+        if (kc.left > 0) {
+          decode(kc, false);
+          walk.next(kc);
+        }
+        decode(vc, true);
+        walk.next(vc);
+      }
+    } else if (warp >= 4) {
+      // ======================= softmax: one query row per thread =======================
+      const int tile = (warp - 4) >> 2;
+      const int r = ((warp & 3) << 5) + lane;            // TMEM lane = row within the tile
+      const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_col = tmem + lane_addr + 128u * tile;
+      const uint32_t o_col = tmem + lane_addr + 256u + 128u * tile;
+      const bool neg = p.qscale < 0.f;
+      float m_ref = -INFINITY, z = 0.f;
+      uint32_t k = 0, seg = 0;                            // blocks of this tile, segments of the CTA
+      int lim = 0;                                        // keys the row sees
+      bool real = false;                                  // the row exists
+      bool first_seg = true, seg_is_first = true, from_zero = false;
+      for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
+        if (c.start) {
+          ++seg;
+          seg_is_first = first_seg;
+          first_seg = false;
+          from_zero = c.j == 0;
+          const int rr = c.it.r0 + tile * TR + r;
+          real = r < TR && rr < c.s.n * G;
+          lim = real ? row_limit(p.t, c.s, rr) : c.s.len;  // rows that do not exist take the unmasked path
+          m_ref = -INFINITY;
+          z = 0.f;
+        }
+        if (walk.tiles(c) <= tile) continue;
+        wait_bar(bar(S_FULL + tile), k & 1u, p.err, abort_flag);
+        tc_fence_after();
+        const int nv = min(kBT, lim - c.j * kBT);
+        // pass 1: the row's extreme over the columns it sees, 64 at a time
+        float mx = neg ? INFINITY : -INFINITY;
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t sr[64];
+          KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
+          KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+          tmem_wait_ld();
+          if (nv < kBT) {
+            const uint32_t fill = __float_as_uint(neg ? INFINITY : -INFINITY);
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (64 * hh + e >= nv) sr[e] = fill;
+          }
+          mx = neg ? fminf(mx, row_extreme<true>(sr)) : fmaxf(mx, row_extreme<false>(sr));
+        }
+        // (a row that sees no column keeps mx = -inf, or +inf under a negative scale: never a new reference)
+        const float mb = nv > 0 ? mx * p.qscale : -INFINITY;
+        const bool need = mb > m_ref + kLazy;
+        const float m_new = need ? mb : m_ref;
+        const float a = need ? ex2(m_ref - m_new) : 1.f;  // 0 on the first block
+        z *= a;
+        m_ref = m_new;
+        if (__any_sync(0xffffffffu, need) && !c.start) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t orr[32];
+            KVQ_LD32(orr, o_col + 32u * cc);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+            KVQ_ST32(o_col + 32u * cc, orr);
+          }
+        }
+        // pass 2: p = exp2(s * qscale - m_ref) as bf16 over the S columns; a
+        // block that every row of the warp sees whole needs no masking
+        const u64 qs2 = pack2(p.qscale, p.qscale), nm2 = pack2(-m_ref, -m_ref);
+        u64 z2 = 0ull;
+        if (__all_sync(0xffffffffu, nv >= kBT)) {
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t sr[32];
+            KVQ_LD32(sr, s_col + 32u * cc);
+            tmem_wait_ld();
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
+              const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
+              z2 = add2(z2, pack2(p0, p1));
+              pk[e] = pack_bf16(p0, p1);
+            }
+            KVQ_ST16(s_col + 16u * cc, pk);
+          }
+        } else {
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t sr[32];
+            KVQ_LD32(sr, s_col + 32u * cc);
+            tmem_wait_ld();
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
+              const float p0 = 32 * cc + 2 * e < nv ? ex2(lo_f(x)) : 0.f;
+              const float p1 = 32 * cc + 2 * e + 1 < nv ? ex2(hi_f(x)) : 0.f;
+              z2 = add2(z2, pack2(p0, p1));
+              pk[e] = pack_bf16(p0, p1);
+            }
+            KVQ_ST16(s_col + 16u * cc, pk);
+          }
+        }
+        z += lo_f(z2) + hi_f(z2);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P_FULL + tile));
+        if (walk.last(c)) {
+          // the segment's last P V product must be done before O is read
+          wait_bar(bar(PV_DONE + tile), k & 1u, p.err, abort_flag);
+          tc_fence_after();
+          const bool whole = from_zero && c.j + 1 == c.nb;
+          const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
+          const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
+          const int rr = c.it.r0 + tile * TR + r;
+          const long long row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
+          const int pr = tile * 128 + r;
+          float* part = p.partials + (2 * static_cast<long long>(blockIdx.x) + (seg_is_first ? 0 : 1)) * 256 * (D + 2) +
+                        static_cast<long long>(pr >> 5) * (D + 2) * 32 + (pr & 31);
+          if (!whole) {
+            part[0] = m_ref;
+            part[32] = z;
+          }
+          // z = 0: a row without a key
+          const float inv = poison ? __uint_as_float(0x7fc00000u) : (z == 0.f ? 0.f : 1.f / z);
+          const float keep = poison ? inv : 1.f;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t orr[32];
+            KVQ_LD32(orr, o_col + 32u * cc);
+            tmem_wait_ld();
+            if (whole) {
+              uint32_t ob[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                ob[e] = pack_bf16(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+              if (real) {
+                uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + 32 * cc);
+#pragma unroll
+                for (int qq = 0; qq < 4; ++qq)
+                  dst[qq] = make_uint4(ob[4 * qq], ob[4 * qq + 1], ob[4 * qq + 2], ob[4 * qq + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) part[(2 + 32 * cc + e) * 32] = __uint_as_float(orr[e]) * keep;
+            }
+          }
+          tc_fence_before();
+        }
+        ++k;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+int tile_tokens(const AttendArgs& a) { return 128 / a.G; }
+// Rows of an item: one tile where no sequence has more, else two.
+int item_rows(const AttendArgs& a) {
+  const int tr = tile_tokens(a) * a.G;
+  return static_cast<long long>(a.max_q) * a.G > tr ? 2 * tr : tr;
+}
+template <int D>
+size_t smem_bytes(const AttendArgs& a) {
+  return 1024 + Smem<D>::kPre + (plan_inline(a, item_rows(a)) ? sizeof(int) * (a.S + 1) : 0);
+}
+size_t smem_of(const AttendArgs& a) { return a.g.D == 64 ? smem_bytes<64>(a) : smem_bytes<128>(a); }
+
+int ctas(const AttendArgs& a) { return a.splits > 0 ? a.splits : (sm_count() > 0 ? sm_count() : 148); }
+
+bool applies(const AttendArgs& a) {
+  return a.g.group == 32 && (a.g.D == 64 || a.g.D == 128) && a.q_dtype == KVQ_BF16 && a.G <= 128 &&
+         static_cast<long long>(a.max_q) * a.G > 16 && smem_of(a) <= 227 * 1024;
+}
+size_t workspace(const AttendArgs& a) {
+  return plan_bytes(a, item_rows(a)) + 2 * static_cast<size_t>(ctas(a)) * 256 * (a.g.D + 2) * sizeof(float);
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link)
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Q as (feature, head of the group, KV head, token); a box is a row tile's
+// half: 64 features x G heads x 1 x TT tokens, rows token-major in shared
+// memory with the 128-byte swizzle the UMMA descriptors expect.  Tokens past T
+// read as zero.
+bool make_q_map(const AttendArgs& a, CUtensorMap* map) {
+  const EncodeTiled enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t D = static_cast<cuuint64_t>(a.g.D), G = static_cast<cuuint64_t>(a.G),
+                   H = static_cast<cuuint64_t>(a.g.H_kv);
+  const cuuint64_t dims[4] = {D, G, H, static_cast<cuuint64_t>(a.T)};
+  const cuuint64_t strides[3] = {D * 2, G * D * 2, H * G * D * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), 1, static_cast<cuuint32_t>(tile_tokens(a))};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.Q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+kvq_status launch(const AttendArgs& a, cudaStream_t s) {
+  const int RI = item_rows(a);
+  CUtensorMap qmap;
+  if (!make_q_map(a, &qmap)) return KVQ_ERR_CUDA;
+  Params p{};
+  p.t = make_batch(a);
+  p.plan = plan_mem(a, RI, a.workspace);
+  p.k_codes = a.k_codes;
+  p.k_scales = a.k_scales;
+  p.v_codes = a.v_codes;
+  p.v_scales = a.v_scales;
+  p.qscale = a.scale * kLog2e;
+  p.O = static_cast<__nv_bfloat16*>(a.O);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan_bytes(a, RI));
+  p.ctas = ctas(a);
+  p.RI = RI;
+  p.TT = tile_tokens(a);
+  p.err = error_word();
+  if (!p.err) return KVQ_ERR_CUDA;
+  if (p.plan.count) {
+    const kvq_status st = launch_plan(a, p.plan, RI, kBT, s);
+    if (st != KVQ_OK) return st;
+  }
+  const size_t smem = smem_of(a);
+  auto kernel = a.g.D == 64 ? (a.g.bits == 4 ? paged_chunk_kernel<4, 64> : paged_chunk_kernel<8, 64>)
+                            : (a.g.bits == 4 ? paged_chunk_kernel<4, 128> : paged_chunk_kernel<8, 128>);
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
+  if (launch_pdl(kernel, dim3(p.ctas), dim3(kThreads), smem, s, qmap, p) != cudaSuccess) return KVQ_ERR_CUDA;
+  count_launch();
+  MergeCall m{};
+  m.t = p.t;
+  m.plan = p.plan;
+  m.items = plan_items(a, RI);
+  m.RI = RI;
+  m.BT = kBT;
+  m.workers = p.ctas;
+  m.D = a.g.D;
+  m.partials = p.partials;
+  m.O = a.O;
+  m.o_dtype = a.q_dtype;
+  m.tile_rows = p.TT * a.G;
+  return launch_merge(m, s);
+}
+
+const AttendImpl kChunk{"paged_chunk_tcgen05", applies, workspace, launch};
+
+}  // namespace
+
+const AttendImpl& chunk_impl() { return kChunk; }
+
+}  // namespace paged
+}  // namespace kvq

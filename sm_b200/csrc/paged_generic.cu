@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(Params p) {
     if (whole) {
       for (int idx = threadIdx.x; idx < rows * D; idx += kThreads) {
         const int r = idx / D;
-        store_from_f32(p.O, q_row(r) * D + idx % D, s_z[r] > 0.f ? s_u[idx] / s_z[r] : 0.f, p.q_dtype);
+        store_from_f32(p.O, q_row(r) * D + idx % D, s_z[r] == 0.f ? 0.f : s_u[idx] / s_z[r], p.q_dtype);
       }
     } else {
       const long long slot = 2 * static_cast<long long>(blockIdx.x) + (g == wr.g0 ? 0 : 1);

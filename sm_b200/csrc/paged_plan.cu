@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(MergeParams p
     const int rr = it.r0 + r;
     const long long o = (static_cast<long long>(s.q0 + rr / c.t.G) * H_q + h * c.t.G + rr % c.t.G) * D + f;
     float M = -INFINITY, Z = 0.f, U = 0.f;
+    bool nan = false;                          // a part whose sum is not a number: neither is the row
     for (int k0 = 0; k0 < q.n; k0 += 32) {
       const int k = k0 + lane;
       float m = -INFINITY, z = 0.f;
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(MergeParams p
         z = mz.y;
         m = z > 0.f ? mz.x : -INFINITY;
       }
+      nan |= __any_sync(0xffffffffu, z != z);
       float top = m;
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -199,7 +201,84 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(MergeParams p
         if (wj > 0.f) U = fmaf(wj, u, U);      // a part without a key holds nothing
       }
     }
-    if (f < D) store_from_f32(c.O, o, Z > 0.f ? U / Z : 0.f, c.o_dtype);
+    if (f < D) store_from_f32(c.O, o, nan ? NAN : (Z > 0.f ? U / Z : 0.f), c.o_dtype);
+  }
+}
+
+// Feature-major partials: one CTA per (item, head), 32-row chunk (blockIdx.y)
+// and 32 features (blockIdx.z); lane = row, a warp takes four features, four
+// parts' loads in flight.
+__global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
+  extern __shared__ int s_pre[];
+  const MergeCall& c = p.c;
+  const int i = blockIdx.x / c.t.H, h = blockIdx.x % c.t.H;
+  if (c.plan.count) griddep_wait();
+  else if (threadIdx.x < 32) warp_prefix(c.t, c.RI, c.BT, s_pre);
+  __syncthreads();
+  const PlanView v = plan_view(c.plan, s_pre, c.t.S);
+  const bool live = i < v.items;
+  const Item it = live ? plan_item(v, i) : Item{0, 0};
+  const SeqView s = seq_view(c.t, it.b);
+  Parts q{};
+  if (live) q = find_parts(c, v, i, it, s, h);
+  if (!c.plan.count) griddep_wait();
+  if (!live) return;
+  if (!c.plan.count && h == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0 && s.bad)
+    record_error(p.err, KVQ_ERR_LENGTH);
+  if (q.n == 1) return;
+  const int lane = threadIdx.x & 31, f = 32 * blockIdx.z + 4 * (threadIdx.x >> 5);
+  const int pr = 32 * blockIdx.y + lane, tile = pr >> 7;               // padded row of the slot
+  const int r = tile * c.tile_rows + (pr & 127);
+  const bool real = (pr & 127) < c.tile_rows && r < q.rows;
+  const int D = c.D;
+  const long long stride = 256LL * (D + 2);
+  const float* base = c.partials + static_cast<long long>(blockIdx.y) * (D + 2) * 32 + lane;
+  float M = -INFINITY, Z = 0.f, U[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int PB = 4;
+  bool nan = false;
+  for (int k0 = 0; k0 < q.n; k0 += PB) {
+    float m[PB], z[PB], u[PB][4];
+#pragma unroll
+    for (int k = 0; k < PB; ++k) {
+      m[k] = -INFINITY;
+      z[k] = 0.f;
+      if (k0 + k < q.n && real) {
+        const float* part = base + part_slot(q, k0 + k) * stride;
+        m[k] = part[0];
+        z[k] = part[32];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[k][e] = part[(2 + f + e) * 32];
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int k = 0; k < PB; ++k) nan |= z[k] != z[k];
+#pragma unroll
+    for (int k = 0; k < PB; ++k)
+      if (z[k] > 0.f) top = fmaxf(top, m[k]);
+    if (top == -INFINITY) continue;
+    const float keep = exp2_w(M - top);
+    M = top;
+    Z *= keep;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) U[e] *= keep;
+#pragma unroll
+    for (int k = 0; k < PB; ++k)
+      if (z[k] > 0.f) {
+        const float w = exp2_w(m[k] - top);
+        Z = fmaf(w, z[k], Z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) U[e] = fmaf(w, u[k][e], U[e]);
+      }
+  }
+  if (real) {
+    const int rr = it.r0 + r;
+    const long long o =
+        (static_cast<long long>(s.q0 + rr / c.t.G) * c.t.H * c.t.G + h * c.t.G + rr % c.t.G) * D + f;
+    const float inv = nan ? NAN : (Z > 0.f ? 1.f / Z : 0.f);
+    __nv_bfloat162 lo = __floats2bfloat162_rn(U[0] * inv, U[1] * inv), hi = __floats2bfloat162_rn(U[2] * inv, U[3] * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(c.O) + o) =
+        make_uint2(*reinterpret_cast<unsigned*>(&lo), *reinterpret_cast<unsigned*>(&hi));
   }
 }
 
@@ -223,6 +302,17 @@ kvq_status launch_merge(const MergeCall& c, cudaStream_t s) {
   const long long grid = c.items * c.t.H;
   if (grid > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   const size_t smem = c.plan.count ? 0 : (static_cast<size_t>(c.t.S) + 1) * sizeof(int);
+  if (c.tile_rows > 0) {
+    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(merge_tiles_kernel), smem)) return KVQ_ERR_CUDA;
+    const int tiles = c.RI > c.tile_rows ? 2 : 1;
+    const int last = c.RI - (tiles - 1) * c.tile_rows;                 // rows of the last tile
+    if (launch_pdl(merge_tiles_kernel,
+                   dim3(static_cast<unsigned>(grid), 4 * (tiles - 1) + (last + 31) / 32, c.D / 32), dim3(256), smem, s,
+                   p) != cudaSuccess)
+      return KVQ_ERR_CUDA;
+    count_launch();
+    return KVQ_OK;
+  }
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(merge_rows_kernel), smem)) return KVQ_ERR_CUDA;
   if (launch_pdl(merge_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(kMergeThreads), smem, s, p) !=
       cudaSuccess)

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
         const int r = 4 * n + c;
         if (r < rows) {
           const int rr = done.it.r0 + r;
-          const float inv = zt > 0.f ? 1.f / zt : 0.f;
+          const float inv = zt == 0.f ? 0.f : 1.f / zt;
           const long long o = (static_cast<long long>(done.s.q0 + rr / G) * H_q + done.h * G + rr % G) * D;
           if (!whole && g == 0) *reinterpret_cast<float2*>(part + C::RI * D + 2 * r) = make_float2(m_ref[n], zt);
           // 4-bit: features 32 ch + 4 g + 0..3; 8-bit: 16 ch + 2 g + 0..1

@@ -6,7 +6,17 @@ score is a sum of 128 products of which the absolute values add up to about 10
 in log2 units for these inputs, so its float32 error is below 128 * 2^-24 * 10
 = 8e-5, and an error d of every score moves an output by at most 2 d max|V|
 ln 2); a bf16 output through its rounding interval at the library's 2e-3 *
-max|V| (gpu_util)."""
+max|V| (gpu_util).  Where the tensor-core kernel of many rows runs, K, V and
+the softmax's p are bf16 tiles, each rounded once (at most 2^-8 of the value):
+V moves an output by at most 2^-8 max|V|, p by as much (a weighted mean of the
+errors), and K through the scores: a score is a sum of 64 or 128 products whose
+independent roundings have a deviation below 2^-8 / sqrt(3) * sqrt(sum (q k
+scale)^2), and for these inputs that root is about 1: 2.3e-3, five deviations
+1.1e-2; an error e of the scores moves an output by at most e max|V| / 2 for
+each of the keys that share the weight, p (1 - p) <= 1/4 and values differing by
+at most 2 max|V|: 2^-7 max|V|.  Together 2^-6 max|V|; and over all outputs the
+four roundings (with the output's own) have relative deviations of at most
+2^-8 / sqrt(3) each, 4.6e-3 together: 6e-3 is asked of the whole."""
 
 from __future__ import annotations
 
@@ -22,6 +32,8 @@ from tests.gpu_util import DEV, bf16_values, check_rows_rounded, to_dev
 pytestmark = pytest.mark.gpu
 
 F32_TOL = 2e-4
+TILE_TOL = 2.0 ** -6
+TILE_REL = 6e-3
 
 
 def i32(x):
@@ -222,6 +234,7 @@ def run_attend(s, news, G, dtype, causal, extra=0, splits=0, max_q=None, scale=N
     out = torch.full((T, H * G, D), 77.0, dtype=dtype, device=DEV)
     K.paged_attend(to_dev(q, dtype), s.cache, i32(s.table), i32(s.lens()), i32(cu), max_q or max(max(news), 1), scale,
                    causal=causal, out=out, splits=splits)
+    out.tiles = K.paged_kernel_name(s.cache, dtype, max_q or max(max(news), 1), H * G) == "paged_chunk_tcgen05"
     want = []
     for b, n in enumerate(news):
         if n:
@@ -232,8 +245,10 @@ def run_attend(s, news, G, dtype, causal, extra=0, splits=0, max_q=None, scale=N
     return out, want, cu
 
 
-def check_attend(out, want, cu, dtype, what=""):
+def check_attend(out, want, cu, dtype, what="", tiles=None):
     o = out.float().cpu().numpy()
+    tiles = out.tiles if tiles is None else tiles
+    off = size = 0.0
     for b, w in enumerate(want):
         if w is None:
             continue
@@ -245,11 +260,13 @@ def check_attend(out, want, cu, dtype, what=""):
             a, r = got[:, h * G:(h + 1) * G], rows[:, h * G:(h + 1) * G]
             top = float(np.abs(vd[h]).max())
             if dtype == torch.bfloat16:
-                check_rows_rounded(a, r, 2e-3 * top, f"{what} b={b} h={h}")
+                check_rows_rounded(a, r, (TILE_TOL if tiles else 2e-3) * top, f"{what} b={b} h={h}")
+                off, size = off + float(np.square(a - r).sum()), size + float(np.square(r).sum())
             else:
                 assert np.isfinite(a).all(), f"{what} b={b} h={h}"
                 err = np.abs(a - r).max()
                 assert err <= F32_TOL * top, f"{what} b={b} h={h}: {err:.3e} > {F32_TOL * top:.3e}"
+    assert not tiles or off <= TILE_REL ** 2 * size, f"{what}: {(off / size) ** 0.5:.2e} of the outputs' norm"
     assert (o[cu[-1]:] == 77.0).all(), f"{what}: rows behind the last sequence"
 
 
@@ -334,6 +351,26 @@ def test_attend_ignores_what_is_past_a_row():
         b, _, _ = run_attend(s, [n], 4, dtype, True, q=q)
         assert torch.equal(a[:n - 1], b[:n - 1])
         assert not torch.isfinite(b[n - 1].float()).all()
+    K.check(DEV)
+
+
+def test_attend_nan_query_gives_nan_rows():
+    """A row whose query is not a number is not one either, split or not, and
+    the other rows are as they were."""
+    rng = np.random.default_rng(14)
+    for D, n, dtype in ((128, 1, torch.bfloat16), (128, 50, torch.bfloat16), (64, 2, torch.float32),
+                        (80, 3, torch.float32)):
+        s = Sequences(rng, [600], 1, D, 4, 32 if D != 80 else 8, 64)
+        s.append([600])
+        q = rng.standard_normal((n, 2, D)).astype(np.float32)
+        for splits in (1, 0):
+            good, _, _ = run_attend(s, [n], 2, dtype, True, q=q, splits=splits)
+            bad_q = q.copy()
+            bad_q[n - 1, 1, 5] = np.nan
+            out, _, _ = run_attend(s, [n], 2, dtype, True, q=bad_q, splits=splits)
+            assert torch.isnan(out[n - 1, 1].float()).all(), (D, n, splits)
+            out[n - 1, 1] = good[n - 1, 1]
+            assert torch.equal(out, good), (D, n, splits)
     K.check(DEV)
 
 
@@ -561,7 +598,8 @@ def test_serving_steps(dtype, D, G, bits, P):
             else:
                 want.append(None)
         s.check_bytes()
-        check_attend(out, want, cu, dtype, str(news))
+        check_attend(out, want, cu, dtype, str(news),
+                     K.paged_kernel_name(s.cache, dtype, max(news), hq) == "paged_chunk_tcgen05")
 
 
 def test_captured_step_replays_on_new_inputs():
@@ -615,7 +653,7 @@ def test_captured_step_replays_on_new_inputs():
             kd, vd = s.decoded(b)
             want.append((R.attend_rows(raw[0][b:b + 1], kd, vd, total[b] + i + 1, 1 / np.sqrt(D), True), vd))
         for o in out:
-            check_attend(o, want, np.arange(S + 1), torch.bfloat16, f"replay {i}")
+            check_attend(o, want, np.arange(S + 1), torch.bfloat16, f"replay {i}", False)
         s.check_bytes()
     K.check(DEV)
 
