@@ -101,30 +101,59 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch t, PlanMem m, 
 struct MergeParams {
   MergeCall c;
   unsigned int* err;
+  int by_item;           // a unit is an (item, head); else a boundary between two workers
+  int units;             // units of the launch; CTAs past them write the rows of items without a key
 };
 
 struct Parts {
+  int i, h;
+  Item it;
+  SeqView s;
   int rows;              // rows of the item
-  long long out0;        // row index of the item's row 0 within O's [T, H_q]
   long long c_first;     // first worker
   int n;                 // workers (0: no key, zero rows)
-  bool first_is_start;   // the first worker's range begins inside (or at) this head's blocks
+  bool first_is_start;   // the first worker's range begins at this head's first block
+  bool mine;             // this unit merges it
 };
 
-// The workers whose ranges meet the blocks of (item, head h).
-__device__ __forceinline__ Parts find_parts(const MergeCall& c, const PlanView& v, int i, const Item& it,
-                                            const SeqView& s, int h) {
-  Parts p{};
-  p.rows = min(c.RI, s.n * c.t.G - it.r0);
-  const int nb = v.pre[i + 1] - v.pre[i];
-  if (nb > 0) {
-    const Range r = worker_range(v, c.t.H, c.workers, 0);
-    const long long S = static_cast<long long>(c.t.H) * v.pre[i] + static_cast<long long>(h) * nb;
-    p.c_first = S / r.per;
-    p.n = static_cast<int>((S + nb - 1) / r.per - p.c_first + 1);
-    p.first_is_start = p.c_first * r.per == S;
+// The (item, head) of a unit and the workers whose ranges meet its blocks.
+// Where there are more (item, head)s than workers, the units are the
+// boundaries between workers: the first boundary inside an (item, head)
+// merges it, and the many that one worker covers cost nothing.
+__device__ __forceinline__ Parts find_parts(const MergeParams& p, const PlanView& v, int unit) {
+  const MergeCall& c = p.c;
+  const int H = c.t.H;
+  Parts q{};
+  const Range r = worker_range(v, H, c.workers, 0);
+  long long start;
+  int nb;
+  if (p.by_item) {
+    q.i = unit / H;
+    q.h = unit % H;
+    if (q.i >= v.items) return q;
+    nb = v.pre[q.i + 1] - v.pre[q.i];
+    start = static_cast<long long>(H) * v.pre[q.i] + static_cast<long long>(q.h) * nb;
+    q.mine = true;
+  } else {
+    const long long x = (unit + 1) * r.per;
+    if (x >= r.total) return q;
+    q.i = find_item(v, H, x);
+    nb = v.pre[q.i + 1] - v.pre[q.i];
+    q.h = static_cast<int>((x - static_cast<long long>(H) * v.pre[q.i]) / nb);
+    start = static_cast<long long>(H) * v.pre[q.i] + static_cast<long long>(q.h) * nb;
+    q.mine = x > start && x - r.per <= start;
+    if (!q.mine) return q;
   }
-  return p;
+  q.it = plan_item(v, q.i);
+  q.s = seq_view(c.t, q.it.b);
+  q.rows = min(c.RI, q.s.n * c.t.G - q.it.r0);
+  if (nb > 0) {
+    q.c_first = start / r.per;
+    q.n = static_cast<int>((start + nb - 1) / r.per - q.c_first + 1);
+    q.first_is_start = q.c_first * r.per == start;
+  }
+  if (q.n == 1) q.mine = false;                // that worker wrote the rows
+  return q;
 }
 
 // Slot of part k: every worker after the first begins inside this head's
@@ -133,103 +162,171 @@ __device__ __forceinline__ long long part_slot(const Parts& p, int k) {
   return 2 * (p.c_first + k) + ((k > 0 || p.first_is_start) ? 0 : 1);
 }
 
+// Row r of item row space within O's [T, H_q] rows.
+__device__ __forceinline__ long long out_row(const MergeCall& c, const Parts& q, int r) {
+  const int rr = q.it.r0 + r;
+  return static_cast<long long>(q.s.q0 + rr / c.t.G) * (c.t.H * c.t.G) + q.h * c.t.G + rr % c.t.G;
+}
+
 __device__ __forceinline__ float exp2_w(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// Row-major partials: one CTA per (item, head); a warp per (row, 32 features).
-constexpr int kMergeThreads = 256;
-__global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(MergeParams p) {
-  extern __shared__ int s_pre[];
-  const MergeCall& c = p.c;
-  const int i = blockIdx.x / c.t.H, h = blockIdx.x % c.t.H;
-  // the inline plan reads only the call's inputs (through the L2), so it runs
-  // while the attention kernel drains
-  if (c.plan.count) griddep_wait();
-  else if (threadIdx.x < 32) warp_prefix(c.t, c.RI, c.BT, s_pre);
-  __syncthreads();
-  const PlanView v = plan_view(c.plan, s_pre, c.t.S);
-  const bool live = i < v.items;
-  const Item it = live ? plan_item(v, i) : Item{0, 0};
-  const SeqView s = seq_view(c.t, it.b);
-  Parts q{};
-  if (live) q = find_parts(c, v, i, it, s, h);
-  if (!c.plan.count) griddep_wait();
-  if (!live) return;
-  if (!c.plan.count && h == 0 && threadIdx.x == 0 && s.bad) record_error(p.err, KVQ_ERR_LENGTH);
-  if (q.n == 1) return;                        // that worker wrote the rows
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int D = c.D, slices = (D + 31) / 32;
-  const long long stride = static_cast<long long>(c.RI) * (D + 2);
-  const int H_q = c.t.H * c.t.G;
-  for (int task = warp; task < q.rows * slices; task += kMergeThreads / 32) {
-    const int r = task / slices, f = (task % slices) * 32 + lane;
-    const int rr = it.r0 + r;
-    const long long o = (static_cast<long long>(s.q0 + rr / c.t.G) * H_q + h * c.t.G + rr % c.t.G) * D + f;
-    float M = -INFINITY, Z = 0.f, U = 0.f;
-    bool nan = false;                          // a part whose sum is not a number: neither is the row
-    for (int k0 = 0; k0 < q.n; k0 += 32) {
-      const int k = k0 + lane;
-      float m = -INFINITY, z = 0.f;
-      if (k < q.n) {
-        const float2 mz = *reinterpret_cast<const float2*>(c.partials + part_slot(q, k) * stride +
-                                                           static_cast<long long>(c.RI) * D + 2 * r);
-        z = mz.y;
-        m = z > 0.f ? mz.x : -INFINITY;
-      }
-      nan |= __any_sync(0xffffffffu, z != z);
-      float top = m;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      top = fmaxf(top, M);
-      if (top == -INFINITY) continue;
-      const float keep = exp2_w(M - top);
-      const float w = exp2_w(m - top);
-      float zs = w * z;
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) zs += __shfl_xor_sync(0xffffffffu, zs, x);
-      M = top;
-      Z = Z * keep + zs;
-      U *= keep;
-      const int n = min(32, q.n - k0);
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-        const float u = f < D ? c.partials[part_slot(q, k0 + j) * stride + static_cast<long long>(r) * D + f] : 0.f;
-        if (wj > 0.f) U = fmaf(wj, u, U);      // a part without a key holds nothing
-      }
+// The plan, the unit's parts (computed by one thread: its 64-bit divisions run
+// once per CTA) and the wait for the attention kernel.  The inline plan reads
+// only the call's inputs (through the L2), so it runs while that kernel
+// drains; the workspace's plan is read after the wait.
+__device__ __forceinline__ PlanView merge_prologue(const MergeParams& p, int unit, int* s_pre, Parts* s_parts) {
+  const bool global = p.c.plan.count != nullptr;
+  if (global) griddep_wait();
+  if (threadIdx.x < 32) {
+    if (!global) warp_prefix(p.c.t, p.c.RI, p.c.BT, s_pre);
+    __syncwarp();
+    if (threadIdx.x == 0) {
+      *s_parts = Parts{};
+      if (unit < p.units) *s_parts = find_parts(p, plan_view(p.c.plan, s_pre, p.c.t.S), unit);
     }
-    if (f < D) store_from_f32(c.O, o, nan ? NAN : (Z > 0.f ? U / Z : 0.f), c.o_dtype);
+  }
+  __syncthreads();
+  if (!global) griddep_wait();
+  return plan_view(p.c.plan, s_pre, p.c.t.S);
+}
+
+// CTA `z` of `nz` that look after what no unit does: zero rows for the items
+// without a key (units by boundary), and the report of bad sequences (inline
+// plan; plan_kernel reports its own).
+__device__ __forceinline__ void odd_jobs(const MergeParams& p, const PlanView& v, int z, int nz) {
+  const MergeCall& c = p.c;
+  if (!c.plan.count)
+    for (int b = z * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); b < c.t.S; b += nz * blockDim.x)
+      if (seq_view(c.t, b).bad) record_error(p.err, KVQ_ERR_LENGTH);
+  if (p.by_item) return;
+  for (int i = z; i < v.items; i += nz) {
+    if (v.pre[i + 1] != v.pre[i]) continue;
+    Parts q{};
+    q.it = plan_item(v, i);
+    q.s = seq_view(c.t, q.it.b);
+    const int rows = min(c.RI, q.s.n * c.t.G - q.it.r0);
+    for (int h = 0; h < c.t.H; ++h) {
+      q.h = h;
+      for (int x = threadIdx.x; x < rows * c.D; x += blockDim.x)
+        store_from_f32(c.O, out_row(c, q, x / c.D) * c.D + x % c.D, 0.f, c.o_dtype);
+    }
   }
 }
 
-// Feature-major partials: one CTA per (item, head), 32-row chunk (blockIdx.y)
-// and 32 features (blockIdx.z); lane = row, a warp takes four features, four
-// parts' loads in flight.
+// Row-major partials: one CTA per unit and row.  Its four warps divide the
+// parts; a warp loads the (m, z) of 32 parts at once (lane = part), then the u
+// rows of its own parts with independent 16-byte loads, eight in flight, and
+// the warps' sums meet in shared memory.  kVec: D a multiple of 4.
+constexpr int kMergeWarps = 4;
+template <bool kVec>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(MergeParams p) {
+  extern __shared__ int s_pre[];
+  __shared__ Parts s_parts;
+  __shared__ float s_u[kMergeWarps][256];
+  const MergeCall& c = p.c;
+  const int unit = blockIdx.x, r = blockIdx.y;
+  const PlanView v = merge_prologue(p, unit, s_pre, &s_parts);
+  if (unit >= p.units) {
+    if (r == 0) odd_jobs(p, v, unit - p.units, gridDim.x - p.units);
+    return;
+  }
+  const Parts q = s_parts;
+  if (!q.mine || r >= q.rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int D = c.D;
+  const long long stride = static_cast<long long>(c.RI) * (D + 2);
+  const float* mz0 = c.partials + static_cast<long long>(c.RI) * D + 2 * r;
+  constexpr int F = 8;                         // features of a lane: 4 lane + 128 j .. + 3, or lane + 32 j
+  float M = -INFINITY, Z = 0.f, U[F];
+  bool nan = false;                            // a part whose sum is not a number: neither is the row
+#pragma unroll
+  for (int j = 0; j < F; ++j) U[j] = 0.f;
+  for (int k0 = 0; k0 < q.n; k0 += 32) {
+    const int k = k0 + lane;
+    float m = -INFINITY, z = 0.f;
+    if (k < q.n) {
+      const float2 mz = *reinterpret_cast<const float2*>(mz0 + part_slot(q, k) * stride);
+      z = mz.y;
+      m = z > 0.f ? mz.x : -INFINITY;
+    }
+    nan |= __any_sync(0xffffffffu, z != z);
+    float top = m;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    top = fmaxf(top, M);
+    if (top == -INFINITY) continue;
+    const float keep = exp2_w(M - top), w = exp2_w(m - top);
+    float zs = w * z;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) zs += __shfl_xor_sync(0xffffffffu, zs, x);
+    M = top;
+    Z = Z * keep + zs;
+#pragma unroll
+    for (int j = 0; j < F; ++j) U[j] *= keep;
+    const int n = min(32, q.n - k0);
+#pragma unroll
+    for (int jj = 0; jj < 32 / kMergeWarps; ++jj) {
+      const int j = jj * kMergeWarps + warp;
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      if (j < n && wj > 0.f) {                 // a part without a key holds nothing
+        const float* u = c.partials + part_slot(q, k0 + j) * stride + static_cast<long long>(r) * D;
+        if (kVec) {
+#pragma unroll
+          for (int e = 0; e < F; e += 4)
+            if (4 * lane + 32 * e < D) {
+              const float4 x = *reinterpret_cast<const float4*>(u + 4 * lane + 32 * e);
+              U[e] = fmaf(wj, x.x, U[e]);
+              U[e + 1] = fmaf(wj, x.y, U[e + 1]);
+              U[e + 2] = fmaf(wj, x.z, U[e + 2]);
+              U[e + 3] = fmaf(wj, x.w, U[e + 3]);
+            }
+        } else {
+#pragma unroll
+          for (int e = 0; e < F; ++e)
+            if (lane + 32 * e < D) U[e] = fmaf(wj, u[lane + 32 * e], U[e]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < F; ++e) {
+    const int f = kVec ? 4 * lane + 128 * (e >> 2) + (e & 3) : lane + 32 * e;
+    if (f < D) s_u[warp][f] = U[e];
+  }
+  __syncthreads();
+  const float inv = nan ? NAN : (Z > 0.f ? 1.f / Z : 0.f);
+  const long long o = out_row(c, q, r) * D;
+  for (int f = threadIdx.x; f < D; f += 32 * kMergeWarps) {
+    float x = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) x += s_u[k][f];
+    store_from_f32(c.O, o + f, x * inv, c.o_dtype);
+  }
+}
+
+// Feature-major partials: one CTA per unit, 32-row chunk (blockIdx.y) and 32
+// features (blockIdx.z); lane = row, a warp takes four features, four parts'
+// loads in flight.
 __global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
   extern __shared__ int s_pre[];
+  __shared__ Parts s_parts;
   const MergeCall& c = p.c;
-  const int i = blockIdx.x / c.t.H, h = blockIdx.x % c.t.H;
-  if (c.plan.count) griddep_wait();
-  else if (threadIdx.x < 32) warp_prefix(c.t, c.RI, c.BT, s_pre);
-  __syncthreads();
-  const PlanView v = plan_view(c.plan, s_pre, c.t.S);
-  const bool live = i < v.items;
-  const Item it = live ? plan_item(v, i) : Item{0, 0};
-  const SeqView s = seq_view(c.t, it.b);
-  Parts q{};
-  if (live) q = find_parts(c, v, i, it, s, h);
-  if (!c.plan.count) griddep_wait();
-  if (!live) return;
-  if (!c.plan.count && h == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0 && s.bad)
-    record_error(p.err, KVQ_ERR_LENGTH);
-  if (q.n == 1) return;
+  const PlanView v = merge_prologue(p, blockIdx.x, s_pre, &s_parts);
+  if (static_cast<int>(blockIdx.x) >= p.units) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) odd_jobs(p, v, blockIdx.x - p.units, gridDim.x - p.units);
+    return;
+  }
+  const Parts q = s_parts;
+  if (!q.mine) return;
   const int lane = threadIdx.x & 31, f = 32 * blockIdx.z + 4 * (threadIdx.x >> 5);
   const int pr = 32 * blockIdx.y + lane, tile = pr >> 7;               // padded row of the slot
   const int r = tile * c.tile_rows + (pr & 127);
   const bool real = (pr & 127) < c.tile_rows && r < q.rows;
+  if (!__any_sync(0xffffffffu, real)) return;
   const int D = c.D;
   const long long stride = 256LL * (D + 2);
   const float* base = c.partials + static_cast<long long>(blockIdx.y) * (D + 2) * 32 + lane;
@@ -272,9 +369,7 @@ __global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
       }
   }
   if (real) {
-    const int rr = it.r0 + r;
-    const long long o =
-        (static_cast<long long>(s.q0 + rr / c.t.G) * c.t.H * c.t.G + h * c.t.G + rr % c.t.G) * D + f;
+    const long long o = out_row(c, q, r) * D + f;
     const float inv = nan ? NAN : (Z > 0.f ? 1.f / Z : 0.f);
     __nv_bfloat162 lo = __floats2bfloat162_rn(U[0] * inv, U[1] * inv), hi = __floats2bfloat162_rn(U[2] * inv, U[3] * inv);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(c.O) + o) =
@@ -297,26 +392,31 @@ kvq_status launch_plan(const AttendArgs& a, const PlanMem& m, int RI, int BT, cu
 }
 
 kvq_status launch_merge(const MergeCall& c, cudaStream_t s) {
-  MergeParams p{c, error_word()};
+  MergeParams p{};
+  p.c = c;
+  p.err = error_word();
   if (!p.err) return KVQ_ERR_CUDA;
-  const long long grid = c.items * c.t.H;
-  if (grid > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  const long long heads = c.items * c.t.H;
+  p.by_item = heads <= c.workers;
+  p.units = p.by_item ? static_cast<int>(heads) : c.workers - 1;
+  // one more CTA reports bad sequences; with units by boundary a few look for
+  // items without a key
+  const unsigned gx = static_cast<unsigned>(p.units) + (p.by_item ? 1 : 16);
   const size_t smem = c.plan.count ? 0 : (static_cast<size_t>(c.t.S) + 1) * sizeof(int);
+  cudaError_t e;
   if (c.tile_rows > 0) {
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(merge_tiles_kernel), smem)) return KVQ_ERR_CUDA;
     const int tiles = c.RI > c.tile_rows ? 2 : 1;
     const int last = c.RI - (tiles - 1) * c.tile_rows;                 // rows of the last tile
-    if (launch_pdl(merge_tiles_kernel,
-                   dim3(static_cast<unsigned>(grid), 4 * (tiles - 1) + (last + 31) / 32, c.D / 32), dim3(256), smem, s,
-                   p) != cudaSuccess)
-      return KVQ_ERR_CUDA;
-    count_launch();
-    return KVQ_OK;
+    e = launch_pdl(merge_tiles_kernel, dim3(gx, 4 * (tiles - 1) + (last + 31) / 32, c.D / 32), dim3(256), smem, s, p);
+  } else {
+    auto kernel = c.D % 4 == 0 ? merge_rows_kernel<true> : merge_rows_kernel<false>;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
+    const long long most = static_cast<long long>(c.t.max_q) * c.t.G;  // rows an item can have
+    e = launch_pdl(kernel, dim3(gx, static_cast<unsigned>(most < c.RI ? most : c.RI)), dim3(32 * kMergeWarps), smem, s,
+                   p);
   }
-  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(merge_rows_kernel), smem)) return KVQ_ERR_CUDA;
-  if (launch_pdl(merge_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(kMergeThreads), smem, s, p) !=
-      cudaSuccess)
-    return KVQ_ERR_CUDA;
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
   count_launch();
   return KVQ_OK;
 }
