@@ -14,6 +14,7 @@
 // call begins in reads the tail slot and the group that it ends in writes it;
 // where these are two groups and both are unfinished, one CTA does them one
 // after the other, so the slot's rows are read before they are replaced.
+#include "f32x2.cuh"
 #include "paged.cuh"
 #include "quant.cuh"
 
@@ -176,26 +177,283 @@ __device__ __forceinline__ void append_group(const AppendParams& p, float* s_x, 
   __syncthreads();
 }
 
+// ---------------------------------------------------------------------------
+// vector form
+// ---------------------------------------------------------------------------
+// Eight features a thread: LPR lanes (a power of two, D / 8 of them used) hold
+// a row, so a row comes with one 16-byte load a lane (two for f32), the partner
+// of a rotation pair is a shuffle away, and a lane's eight codes leave as one
+// word or two.  K and V have CTAs of their own (blockIdx.z): half the
+// registers, twice the loads in flight.  A K CTA holds the group's rows in
+// registers, PASS rows a thread; a channel's maximum goes over the thread's
+// rows, the warp's and (through shared memory) the four warps'.  Arithmetic is
+// on pairs (f32x2).  Needs D and the pairs' distance in whole vectors, groups
+// of 8 to 64 whose features divide D, and aligned rows; append_group above
+// takes the rest.
+constexpr float kRound = 12582912.f;               // 1.5 * 2^23: x + kRound has rint(x) in its low bits
+
+// Eight floats as four pairs.
+struct Eight {
+  u64 v[4];
+  __device__ __forceinline__ float at(int k) const { return k & 1 ? hi_f(v[k >> 1]) : lo_f(v[k >> 1]); }
+};
+__device__ __forceinline__ Eight zero8() { return Eight{{0ull, 0ull, 0ull, 0ull}}; }
+__device__ __forceinline__ Eight load8f(const float* p) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = *reinterpret_cast<const ulonglong2*>(p + 4);
+  return Eight{{a.x, a.y, b.x, b.y}};
+}
+__device__ __forceinline__ void store8f(float* p, const Eight& x) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.v[0], x.v[1]);
+  *reinterpret_cast<ulonglong2*>(p + 4) = make_ulonglong2(x.v[2], x.v[3]);
+}
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendParams p) {
+__device__ __forceinline__ Eight load8(const void* p, long long i) {
+  if (!kBf16) return load8f(static_cast<const float*>(p) + i);
+  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+  const unsigned w[4] = {v.x, v.y, v.z, v.w};
+  Eight x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x.v[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+  return x;
+}
+// The larger of a and |b|; not a number if either is not.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ u64 neg2(u64 a) { return a ^ 0x8000000080000000ull; }
+
+// Quantizes eight values (scale s[k], reciprocal rs[k]) and stores their codes
+// at flat code index i, a multiple of 8.  x / s is taken as x * rs away from a
+// rounding tie (quant.cuh); the sum with kRound leaves rint(x / s) in its low
+// bits, so the codes of a word add up as integers: sum over k of bits_k *
+// 2^(bits k), corrected by one constant.
+__device__ __forceinline__ void quantize8(uint8_t* out, long long i, const Eight& x, const Eight& s, const Eight& rs,
+                                          int bits) {
+  const u64 r2 = pack2(kRound, kRound), n2 = pack2(-kRound, -kRound);
+  u64 t[4];
+  float worst = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const u64 qa = mul2(x.v[k], rs.v[k]);
+    t[k] = add2(qa, r2);
+    const u64 d = add2(qa, neg2(add2(t[k], n2)));
+    worst = max_abs_nan(max_abs_nan(worst, lo_f(d)), hi_f(d));
+  }
+  if (!(worst < 0.5f - 0.000244140625f)) {          // next to a tie, or 1 / s overflowed: quant_code decides
+    const int qmax = bits == 4 ? 7 : 127;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c0 = static_cast<int>(quant_code(lo_f(x.v[k]), lo_f(s.v[k]), lo_f(rs.v[k]), qmax)) - qmax;
+      const int c1 = static_cast<int>(quant_code(hi_f(x.v[k]), hi_f(s.v[k]), hi_f(rs.v[k]), qmax)) - qmax;
+      t[k] = pack2(__uint_as_float(0x4B400000u + c0), __uint_as_float(0x4B400000u + c1));
+    }
+  }
+  auto b = [&](int k) { return static_cast<unsigned>(t[k >> 1] >> (32 * (k & 1))); };
+  if (bits == 4) {
+    unsigned w = 0x77777777u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w += b(k) << (4 * k);
+    *reinterpret_cast<unsigned*>(out + i / 2) = w;
+  } else {
+    unsigned w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w[j] = 0x7F7F7F7Fu - 0x4B400000u * 0x01010101u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[j] += b(4 * j + k) << (8 * k);
+    }
+    *reinterpret_cast<uint2*>(out + i) = make_uint2(w[0], w[1]);
+  }
+}
+
+// A group's place in the pages and in the call.
+struct GroupAt {
+  int tok0, first, len, row0;
+};
+
+template <bool kBf16, int LPR, int PASS>
+__device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max, int h, const GroupAt& a,
+                                             const int32_t* table, float* tail) {
+  constexpr int RPP = kThreads / LPR;              // rows of a pass
+  const int g = p.group, D = p.D;
+  const int qmax = p.bits == 4 ? 7 : 127;
+  const int warp = threadIdx.x >> 5;
+  const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR, d0 = 8 * l;
+  const bool on = l < D / 8;
+  const int live = min(g, a.len - a.tok0), kept = max(0, a.first - a.tok0);
+  int page = __ldg(table + a.tok0 / p.P);
+  Eight x[PASS];
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) {
+    const int r = q * RPP + slot;
+    x[q] = zero8();
+    if (on && r < live) {
+      if (r < kept) x[q] = load8f(tail + r * D + d0);
+      else x[q] = load8<kBf16>(p.K, (a.row0 + a.tok0 + r - a.first) * p.k_stride + static_cast<long long>(h) * D + d0);
+    }
+  }
+  if (p.rot > 0) {
+    const int half = p.rot / 2;
+    const bool turns = on && d0 < p.rot, upper = !p.interleaved && d0 >= half;
+    const int lane = threadIdx.x & 31;
+    const int partner = p.interleaved || !turns ? lane : (upper ? lane - half / 8 : lane + half / 8);
+#pragma unroll
+    for (int q = 0; q < PASS; ++q) {
+      const int r = q * RPP + slot, pos = a.tok0 + r;
+      const bool fresh = r >= kept && r < live, turn = turns && fresh && pos < p.n_pos;
+      if (fresh && pos >= p.n_pos && l == 0 && h == 0) record_error(p.err, KVQ_ERR_INDEX);
+      Eight o;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o.v[k] = p.interleaved ? (x[q].v[k] << 32 | x[q].v[k] >> 32) : __shfl_sync(0xffffffffu, x[q].v[k], partner);
+      if (turn) {
+        // a pair's first feature becomes x c - y s, its second y c + x s
+        const float* tab = p.rope + static_cast<long long>(pos) * p.rot;
+        Eight c, s;
+        if (p.interleaved) {
+          const float4 cv = __ldg(reinterpret_cast<const float4*>(tab + d0 / 2));
+          const float4 sv = __ldg(reinterpret_cast<const float4*>(tab + half + d0 / 2));
+          const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            c.v[k] = pack2(cc[k], cc[k]);
+            s.v[k] = pack2(-ss[k], ss[k]);
+          }
+        } else {
+          const int e = upper ? d0 - half : d0;
+          c = load8f(tab + e);
+          s = load8f(tab + half + e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s.v[k] = upper ? s.v[k] : neg2(s.v[k]);
+        }
+        // (-s) y added is s y subtracted, bit for bit; scalar operations, since
+        // a packed product and sum may become one rounding
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[q].v[k] = pack2(__fadd_rn(__fmul_rn(x[q].at(2 * k), c.at(2 * k)), __fmul_rn(o.at(2 * k), s.at(2 * k))),
+                            __fadd_rn(__fmul_rn(x[q].at(2 * k + 1), c.at(2 * k + 1)),
+                                      __fmul_rn(o.at(2 * k + 1), s.at(2 * k + 1))));
+      }
+    }
+  }
+  if (live < g) {                                  // an unfinished group: its new rows are kept
+#pragma unroll
+    for (int q = 0; q < PASS; ++q) {
+      const int r = q * RPP + slot;
+      if (on && r >= kept && r < live) store8f(tail + r * D + d0, x[q]);
+    }
+  }
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
+    if (threadIdx.x == 0) record_error(p.err, KVQ_ERR_INDEX);
+    return;
+  }
+  // a channel's maximum over the group's rows
+  float top[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    top[k] = 0.f;
+#pragma unroll
+    for (int q = 0; q < PASS; ++q) top[k] = fmaxf(top[k], fabsf(x[q].at(k)));
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
+  }
+  if (on && (threadIdx.x & 31) < LPR) {
+    *reinterpret_cast<float4*>(s_max + warp * D + d0) = make_float4(top[0], top[1], top[2], top[3]);
+    *reinterpret_cast<float4*>(s_max + warp * D + d0 + 4) = make_float4(top[4], top[5], top[6], top[7]);
+  }
+  __syncthreads();
+  // a thread turns one channel's maximum into its scale (D <= 256: two a thread)
+  const long long head = static_cast<long long>(page) * p.H + h;
+  const int in_page = a.tok0 % p.P;
+  float* s_scale = s_max + 4 * D;                  // [D], then the reciprocals
+  for (int d = threadIdx.x; d < D; d += kThreads) {
+    const float m = fmaxf(fmaxf(s_max[d], s_max[D + d]), fmaxf(s_max[2 * D + d], s_max[3 * D + d]));
+    const float sc = group_scale(m, qmax);
+    s_scale[d] = sc;
+    s_scale[D + d] = __frcp_rn(sc);
+    p.k_scales[head * p.k_scales_head + static_cast<long long>(in_page / g) * D + d] = sc;
+  }
+  __syncthreads();
+  if (!on) return;
+  const Eight sc = load8f(s_scale + d0), rs = load8f(s_scale + D + d0);
+  uint8_t* out = p.k_codes + head * p.k_codes_head;
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) {
+    const int r = q * RPP + slot;
+    if (r < g) quantize8(out, static_cast<long long>(in_page + r) * D + d0, x[q], sc, rs, p.bits);
+  }
+}
+
+// V rows of the group's new tokens: a group of g features is g / 8 neighbouring
+// lanes of the row.
+template <bool kBf16, int LPR, int PASS>
+__device__ __forceinline__ void append_v_vec(const AppendParams& p, int h, const GroupAt& a, const int32_t* table) {
+  constexpr int RPP = kThreads / LPR;
+  const int g = p.group, D = p.D;
+  const int qmax = p.bits == 4 ? 7 : 127;
+  const int l = threadIdx.x % LPR, slot = threadIdx.x / LPR, d0 = 8 * l;
+  const bool on = l < D / 8;
+  const int live = min(g, a.len - a.tok0), kept = max(0, a.first - a.tok0);
+  const int page = __ldg(table + a.tok0 / p.P);
+  Eight x[PASS];
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) {
+    const int r = q * RPP + slot;
+    x[q] = zero8();
+    if (on && r >= kept && r < live)
+      x[q] = load8<kBf16>(p.V, (a.row0 + a.tok0 + r - a.first) * p.v_stride + static_cast<long long>(h) * D + d0);
+  }
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) return;   // the K CTA records it
+  const long long head = static_cast<long long>(page) * p.H + h;
+  const int in_page = a.tok0 % p.P;
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) {
+    const int r = q * RPP + slot;
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[q].at(k)));
+    for (int o = 1; o < g / 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (on && r >= kept && r < live) {
+      const float sc = group_scale(m, qmax), rs = __frcp_rn(sc);
+      const long long tok = in_page + r;
+      if (d0 % g == 0) p.v_scales[head * p.v_scales_head + tok * (D / g) + d0 / g] = sc;
+      Eight s8, r8;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s8.v[k] = pack2(sc, sc);
+        r8.v[k] = pack2(rs, rs);
+      }
+      quantize8(p.v_codes + head * p.v_codes_head, tok * D + d0, x[q], s8, r8, p.bits);
+    }
+  }
+}
+
+template <bool kBf16, int LPR, int PASS>
+__global__ void __launch_bounds__(kThreads, LPR == 0 || PASS == 8 ? 3 : 6) paged_append_kernel(AppendParams p) {
   griddep_wait();
-  extern __shared__ __align__(16) float s_x[];      // [g][D], scale[D], 1/scale[D]
+  // LPR = 0: append_group's [g][D], scale[D], 1/scale[D]; else [4 warps][D]
+  // maxima, scale[D], 1/scale[D]
+  extern __shared__ __align__(16) float s_x[];
   const long long u = blockIdx.x;
   const int h = blockIdx.y, g = p.group;
+  const bool v_part = blockIdx.z != 0;              // K has a CTA of its own (LPR > 0)
   const int b = p.max_new == 1 ? static_cast<int>(u)
                                : warp_find(p.S, u, [&](int i) { return unit_base(p.cu, i, p.T, g); });
-  const int j = p.max_new == 1 ? 0 : static_cast<int>(u - unit_base(p.cu, b, p.T, g));
-  if (j < 0) return;                                // before the first sequence's rows
+  // one round of loads
+  const int c0 = __ldcg(p.cu + b), len = __ldg(p.lengths + b);
   const RowRange rr = row_range(p.cu, b, p.T, p.max_new);
-  const bool report = threadIdx.x == 0 && j == 0 && h == 0;
+  const int slot = p.slots ? __ldg(p.slots + b) : b;
+  const int j = p.max_new == 1 ? 0 : static_cast<int>(u - (min(max(c0, 0), p.T) / g + 2LL * b));
+  if (j < 0) return;                                // before the first sequence's rows
+  const bool report = threadIdx.x == 0 && j == 0 && h == 0 && !v_part;
   if (rr.bad && report) record_error(p.err, KVQ_ERR_LENGTH);
   if (rr.n == 0) return;
-  const int len = __ldg(p.lengths + b);
   if (len < rr.n || len > p.cap) {
     if (report) record_error(p.err, KVQ_ERR_LENGTH);
     return;
   }
-  const int slot = p.slots ? __ldg(p.slots + b) : b;
   if (static_cast<unsigned>(slot) >= static_cast<unsigned>(p.tail_slots)) {
     if (report) record_error(p.err, KVQ_ERR_INDEX);
     return;
@@ -203,18 +461,30 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendParams p) 
   const int first = len - rr.n;
   const int j0 = first / g, last = (len - 1) / g - j0;
   if (j > last) return;
+  const int32_t* table = p.table + static_cast<long long>(b) * p.max_pages;
+  if constexpr (LPR > 0) {
+    if (v_part) {
+      append_v_vec<kBf16, LPR, PASS>(p, h, GroupAt{(j0 + j) * g, first, len, rr.r0}, table);
+      return;
+    }
+  }
   // both ends unfinished: the CTA of the first group does the last one too
   const bool joined = last > 0 && first % g != 0 && len % g != 0;
   if (joined && j == last) return;
   float* tail = p.tail + (static_cast<long long>(slot) * p.H + h) * g * p.D;
   for (int k = j; k <= last; k += joined && j == 0 ? last : last + 1) {
-    const int tok0 = (j0 + k) * g;
-    int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + tok0 / p.P);
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
-      if (threadIdx.x == 0) record_error(p.err, KVQ_ERR_INDEX);
-      page = -1;
+    const GroupAt at{(j0 + k) * g, first, len, rr.r0};
+    if constexpr (LPR == 0) {
+      int page = __ldg(table + at.tok0 / p.P);
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
+        if (threadIdx.x == 0) record_error(p.err, KVQ_ERR_INDEX);
+        page = -1;
+      }
+      append_group<kBf16>(p, s_x, h, at.tok0, first, len, rr.r0, page, tail);
+    } else {
+      append_k_vec<kBf16, LPR, PASS>(p, s_x, h, at, table, tail);
+      __syncthreads();                              // the tail rows were read, the shared maxima too
     }
-    append_group<kBf16>(p, s_x, h, tok0, first, len, rr.r0, page, tail);
   }
 }
 
@@ -244,34 +514,96 @@ __device__ __forceinline__ float value_at(const uint8_t* codes, long long flat, 
   return __fmul_rn(static_cast<float>(c), scale);
 }
 
-// One warp per row.
-__global__ void __launch_bounds__(kThreads) paged_gather_kernel(GatherParams p) {
+// Four consecutive codes from flat index i (a multiple of 4) less qmax.
+__device__ __forceinline__ void codes4(const uint8_t* codes, long long i, int bits, float (&c)[4]) {
+  if (bits == 8) {
+    const unsigned w = *reinterpret_cast<const unsigned*>(codes + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = static_cast<float>(static_cast<int>((w >> (8 * k)) & 255u) - 127);
+  } else {
+    const unsigned w = *reinterpret_cast<const unsigned short*>(codes + i / 2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = static_cast<float>(static_cast<int>((w >> (4 * k)) & 15u) - 7);
+  }
+}
+__device__ __forceinline__ void store4(void* p, long long i, const float (&x)[4], int dtype) {
+  if (dtype == KVQ_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
+        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+  }
+}
+
+// A CTA takes kGatherRows rows: a warp finds each row's page, then a thread
+// takes four features of one head (kVec; else one) of all the rows, so the
+// loads of the rows do not wait for one another.
+constexpr int kGatherRows = 4, kGatherThreads = 256;
+template <bool kVec>
+__global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(GatherParams p) {
   griddep_wait();
-  const long long row = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  if (row >= p.T) return;
-  const int lane = threadIdx.x & 31;
-  const int b = warp_find(p.S, row, [&](int i) { return row_base(p.cu, i, p.T); });
-  const RowRange rr = row_range(p.cu, b, p.T, p.max_rows);
-  if (lane == 0 && rr.bad) record_error(p.err, KVQ_ERR_LENGTH);
-  if (row < rr.r0 || row >= rr.r0 + rr.n) return;   // no sequence's row
-  const int start = __ldg(p.starts + b);
-  const long long tok = static_cast<long long>(start) + (row - rr.r0);
-  const bool in = start >= 0 && tok < p.cap;
-  if (!in && lane == 0) record_error(p.err, KVQ_ERR_LENGTH);
-  const int page =
-      in ? read_page(__ldg(p.table + static_cast<long long>(b) * p.max_pages + tok / p.P), p.pages, p.err) : 0;
-  const long long at = in ? tok % p.P : 0;
-  for (int i = lane; i < p.H * p.D; i += 32) {
-    const int h = i / p.D, d = i % p.D;
-    const long long head = static_cast<long long>(page) * p.H + h;
-    const long long o = row * p.H * p.D + i;
-    if (p.K) {
-      const float s = p.k_scales[head * p.k_scales_head + (at / p.group) * p.D + d];
-      store_from_f32(p.K, o, in ? value_at(p.k_codes + head * p.k_codes_head, at * p.D + d, p.bits, s) : 0.f, p.dtype);
+  __shared__ int s_page[kGatherRows], s_at[kGatherRows];
+  const long long row0 = static_cast<long long>(blockIdx.x) * kGatherRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < kGatherRows) {
+    const long long row = row0 + warp;
+    int page = -1, at = -1;                         // at < 0: a zero row; page < 0: no sequence's row
+    if (row < p.T) {
+      const int b = warp_find(p.S, row, [&](int i) { return row_base(p.cu, i, p.T); });
+      const RowRange rr = row_range(p.cu, b, p.T, p.max_rows);
+      if (lane == 0 && rr.bad) record_error(p.err, KVQ_ERR_LENGTH);
+      if (row >= rr.r0 && row < rr.r0 + rr.n) {
+        const int start = __ldg(p.starts + b);
+        const long long tok = static_cast<long long>(start) + (row - rr.r0);
+        page = 0;
+        if (start >= 0 && tok < p.cap) {
+          page = read_page(__ldg(p.table + static_cast<long long>(b) * p.max_pages + tok / p.P), p.pages, p.err);
+          at = static_cast<int>(tok % p.P);
+        } else if (lane == 0) {
+          record_error(p.err, KVQ_ERR_LENGTH);
+        }
+      }
     }
-    if (p.V) {
-      const float s = p.v_scales[head * p.v_scales_head + at * (p.Dp / p.group) + d / p.group];
-      store_from_f32(p.V, o, in ? value_at(p.v_codes + head * p.v_codes_head, at * p.Dp + d, p.bits, s) : 0.f, p.dtype);
+    if (lane == 0) {
+      s_page[warp] = page;
+      s_at[warp] = at;
+    }
+  }
+  __syncthreads();
+  constexpr int W = kVec ? 4 : 1;
+  const int per_head = p.D / W, width = p.H * p.D;
+  for (int i = threadIdx.x; i < p.H * per_head; i += kGatherThreads) {
+    const int h = i / per_head, d = (i - h * per_head) * W;
+#pragma unroll
+    for (int k = 0; k < kGatherRows; ++k) {
+      const int page = s_page[k], at = s_at[k];
+      if (page < 0) continue;
+      const long long head = static_cast<long long>(page) * p.H + h;
+      const long long o = (row0 + k) * width + h * p.D + d;
+      const long long t = max(at, 0);
+      const float* ks = p.k_scales + head * p.k_scales_head + (t / p.group) * p.D + d;
+      const float* vs = p.v_scales + head * p.v_scales_head + t * (p.Dp / p.group) + d / p.group;
+      if constexpr (kVec) {
+        float kc[4], vc[4];
+        codes4(p.k_codes + head * p.k_codes_head, t * p.D + d, p.bits, kc);
+        codes4(p.v_codes + head * p.v_codes_head, t * p.Dp + d, p.bits, vc);
+        const float4 s4 = *reinterpret_cast<const float4*>(ks);
+        const float sv = *vs;
+        float ko[4] = {__fmul_rn(kc[0], s4.x), __fmul_rn(kc[1], s4.y), __fmul_rn(kc[2], s4.z), __fmul_rn(kc[3], s4.w)};
+        float vo[4] = {__fmul_rn(vc[0], sv), __fmul_rn(vc[1], sv), __fmul_rn(vc[2], sv), __fmul_rn(vc[3], sv)};
+        if (at < 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ko[e] = vo[e] = 0.f;
+        }
+        if (p.K) store4(p.K, o, ko, p.dtype);
+        if (p.V) store4(p.V, o, vo, p.dtype);
+      } else {
+        const float kv = value_at(p.k_codes + head * p.k_codes_head, t * p.D + d, p.bits, *ks);
+        const float vv = value_at(p.v_codes + head * p.v_codes_head, t * p.Dp + d, p.bits, *vs);
+        if (p.K) store_from_f32(p.K, o, at >= 0 ? kv : 0.f, p.dtype);
+        if (p.V) store_from_f32(p.V, o, at >= 0 ? vv : 0.f, p.dtype);
+      }
     }
   }
 }
@@ -291,6 +623,32 @@ void fill_geometry(const Geometry& g, int max_pages, P* p) {
   p->k_scales_head = static_cast<long long>(g.k_scales_head);
   p->v_codes_head = static_cast<long long>(g.v_codes_head);
   p->v_scales_head = static_cast<long long>(g.v_scales_head);
+}
+
+// Whether the vector form's conditions hold.
+bool vector_form(const AppendCall& a) {
+  const int D = a.g.D, g = a.g.group;
+  const size_t es = a.in_dtype == KVQ_BF16 ? 2 : 4;
+  auto aligned = [&](const void* p, long long stride) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && static_cast<size_t>(stride) * es % 16 == 0;
+  };
+  if (D % 8 != 0 || D < 8 || D > 256 || g < 8 || (g & (g - 1)) != 0 || D % g != 0) return false;
+  if (!aligned(a.K, a.k_stride) || !aligned(a.V, a.v_stride)) return false;
+  if (!a.rope.table) return true;
+  // whole vectors of pairs, and 16-byte rows of the table
+  return a.rope.rot_dim % (a.rope.interleaved ? 8 : 16) == 0 && reinterpret_cast<uintptr_t>(a.rope.table) % 16 == 0;
+}
+
+template <bool kBf16>
+auto pick_append(int lpr, int pass) -> void (*)(AppendParams) {
+  if (pass == 1 && lpr == 8) return paged_append_kernel<kBf16, 8, 1>;
+  if (pass == 1 && lpr == 16) return paged_append_kernel<kBf16, 16, 1>;
+  if (pass == 2 && lpr == 8) return paged_append_kernel<kBf16, 8, 2>;
+  if (pass == 2 && lpr == 16) return paged_append_kernel<kBf16, 16, 2>;
+  if (pass == 2 && lpr == 32) return paged_append_kernel<kBf16, 32, 2>;
+  if (pass == 4 && lpr == 16) return paged_append_kernel<kBf16, 16, 4>;
+  if (pass == 8 && lpr == 32) return paged_append_kernel<kBf16, 32, 8>;
+  return nullptr;
 }
 
 }  // namespace
@@ -324,10 +682,23 @@ kvq_status launch_append(const AppendCall& a, cudaStream_t s) {
   if (!p.err) return KVQ_ERR_CUDA;
   const long long units = a.max_new == 1 ? a.S : static_cast<long long>(a.T) / a.g.group + 2LL * a.S;
   if (units > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
-  const size_t smem = (static_cast<size_t>(a.g.group) * a.g.D + 2 * a.g.D) * sizeof(float);
-  auto kernel = a.in_dtype == KVQ_BF16 ? paged_append_kernel<true> : paged_append_kernel<false>;
+  void (*kernel)(AppendParams) = nullptr;
+  size_t smem = 6 * static_cast<size_t>(a.g.D) * sizeof(float);
+  unsigned parts = 2;                               // K and V
+  int pass = 0, lpr = 8;
+  if (vector_form(a)) {
+    while (8 * lpr < a.g.D) lpr *= 2;
+    pass = (a.g.group + kThreads / lpr - 1) / (kThreads / lpr);
+  }
+  if (a.in_dtype == KVQ_BF16) kernel = pick_append<true>(lpr, pass);
+  else kernel = pick_append<false>(lpr, pass);
+  if (!kernel) {
+    kernel = a.in_dtype == KVQ_BF16 ? paged_append_kernel<true, 0, 0> : paged_append_kernel<false, 0, 0>;
+    smem = (static_cast<size_t>(a.g.group) * a.g.D + 2 * a.g.D) * sizeof(float);
+    parts = 1;
+  }
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
-  if (launch_pdl(kernel, dim3(static_cast<unsigned>(units), a.g.H_kv), dim3(kThreads), smem, s, p) != cudaSuccess)
+  if (launch_pdl(kernel, dim3(static_cast<unsigned>(units), a.g.H_kv, parts), dim3(kThreads), smem, s, p) != cudaSuccess)
     return KVQ_ERR_CUDA;
   count_launch();
   return KVQ_OK;
@@ -351,8 +722,9 @@ kvq_status launch_gather(const GatherCall& a, cudaStream_t s) {
   p.dtype = a.out_dtype;
   p.err = error_word();
   if (!p.err) return KVQ_ERR_CUDA;
-  const int warps = kThreads / 32;
-  if (launch_pdl(paged_gather_kernel, dim3((a.T + warps - 1) / warps), dim3(kThreads), 0, s, p) != cudaSuccess)
+  // four features together: codes in one load, one V scale
+  auto kernel = a.g.D % 4 == 0 && a.g.group % 4 == 0 ? paged_gather_kernel<true> : paged_gather_kernel<false>;
+  if (launch_pdl(kernel, dim3((a.T + kGatherRows - 1) / kGatherRows), dim3(kGatherThreads), 0, s, p) != cudaSuccess)
     return KVQ_ERR_CUDA;
   count_launch();
   return KVQ_OK;
