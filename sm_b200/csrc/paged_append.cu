@@ -29,8 +29,12 @@ constexpr int kThreads = 128;
 // before b touch (a sequence of n tokens touches at most n / g + 2, and
 // floor((c + n) / g) - floor(c / g) >= floor(n / g)), which needs no sum over
 // the sequences.  With at most one token a sequence, base(b) = b.
-__device__ __forceinline__ long long unit_base(const int32_t* cu, int b, int T, int per) {
-  return min(max(__ldcg(cu + b), 0), T) / per + 2LL * b;
+struct GroupSize {
+  int g, lg;                       // lg: its logarithm where it is a power of two, else -1
+  __device__ __forceinline__ int div(int x) const { return lg >= 0 ? x >> lg : x / g; }
+};
+__device__ __forceinline__ long long unit_base(const int32_t* cu, int b, int T, const GroupSize& gs) {
+  return gs.div(min(max(__ldcg(cu + b), 0), T)) + 2LL * b;
 }
 // The same for rows: base(b) = cu[b].
 __device__ __forceinline__ long long row_base(const int32_t* cu, int b, int T) {
@@ -67,7 +71,7 @@ struct AppendParams {
   int S, T, max_new;
   const float* rope;               // [n_pos][rot]
   int n_pos, rot, interleaved;
-  int bits, group, D, Dp, H, P, pages, cap;
+  int bits, group, lg, D, Dp, H, P, pages, cap;    // lg: log2 of the group, or -1
   long long k_codes_head, k_scales_head, v_codes_head, v_scales_head;
   uint8_t* k_codes;
   float* k_scales;
@@ -216,45 +220,47 @@ __device__ __forceinline__ Eight load8(const void* p, long long i) {
   for (int k = 0; k < 4; ++k) x.v[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
   return x;
 }
-// The larger of a and |b|; not a number if either is not.
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
-  return r;
-}
 __device__ __forceinline__ u64 neg2(u64 a) { return a ^ 0x8000000080000000ull; }
 
-// Quantizes eight values (scale s[k], reciprocal rs[k]) and stores their codes
-// at flat code index i, a multiple of 8.  x / s is taken as x * rs away from a
-// rounding tie (quant.cuh); the sum with kRound leaves rint(x / s) in its low
-// bits, so the codes of a word add up as integers: sum over k of bits_k *
-// 2^(bits k), corrected by one constant.
+// Whether quantize8's fast form holds for a scale: 1 / s, and the residuals of
+// quotients up to 127, stay clear of overflow and of denormals.
+__device__ __forceinline__ bool plain_scale(float s) { return s > 1e-28f && s < 1e28f; }
+
+// Quantizes eight values (scale s, reciprocal rs = 1 / s rounded to nearest)
+// and stores their codes at flat code index i, a multiple of 8.
+// The codes are rint of the quotient rounded to f32 (quant.cuh).  That quotient
+// comes without a division from Markstein's theorem (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): if q is
+// within an ulp of x / s and r = x - q s is exact, q + r rs rounds to the
+// rounded quotient; x rs is within two ulps, the first correction brings it
+// within one.  Adding kRound leaves rint in the sum's low bits, so the codes of
+// a word add up as integers: sum over k of bits_k * 2^(bits k), corrected by
+// one constant.  Values that are not finite, and scales outside plain_scale,
+// take quant_code.
 __device__ __forceinline__ void quantize8(uint8_t* out, long long i, const Eight& x, const Eight& s, const Eight& rs,
-                                          int bits) {
-  const u64 r2 = pack2(kRound, kRound), n2 = pack2(-kRound, -kRound);
-  u64 t[4];
-  float worst = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const u64 qa = mul2(x.v[k], rs.v[k]);
-    t[k] = add2(qa, r2);
-    const u64 d = add2(qa, neg2(add2(t[k], n2)));
-    worst = max_abs_nan(max_abs_nan(worst, lo_f(d)), hi_f(d));
-  }
-  if (!(worst < 0.5f - 0.000244140625f)) {          // next to a tie, or 1 / s overflowed: quant_code decides
-    const int qmax = bits == 4 ? 7 : 127;
+                                          int bits, bool plain) {
+  const u64 r2 = pack2(kRound, kRound);
+  unsigned b[8];
+  if (plain) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int c0 = static_cast<int>(quant_code(lo_f(x.v[k]), lo_f(s.v[k]), lo_f(rs.v[k]), qmax)) - qmax;
-      const int c1 = static_cast<int>(quant_code(hi_f(x.v[k]), hi_f(s.v[k]), hi_f(rs.v[k]), qmax)) - qmax;
-      t[k] = pack2(__uint_as_float(0x4B400000u + c0), __uint_as_float(0x4B400000u + c1));
+      const u64 ms = neg2(s.v[k]);
+      u64 q = mul2(x.v[k], rs.v[k]);
+      q = fma2(fma2(q, ms, x.v[k]), rs.v[k], q);
+      q = fma2(fma2(q, ms, x.v[k]), rs.v[k], q);
+      const u64 t = add2(q, r2);
+      b[2 * k] = static_cast<unsigned>(t);
+      b[2 * k + 1] = static_cast<unsigned>(t >> 32);
     }
+  } else {
+    const int qmax = bits == 4 ? 7 : 127;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = 0x4B400000u + quant_code(x.at(k), s.at(k), __frcp_rn(s.at(k)), qmax) - qmax;
   }
-  auto b = [&](int k) { return static_cast<unsigned>(t[k >> 1] >> (32 * (k & 1))); };
   if (bits == 4) {
     unsigned w = 0x77777777u - 0x4B400000u * 0x11111111u;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w += b(k) << (4 * k);
+    for (int k = 0; k < 8; ++k) w += b[k] << (4 * k);
     *reinterpret_cast<unsigned*>(out + i / 2) = w;
   } else {
     unsigned w[2];
@@ -262,11 +268,14 @@ __device__ __forceinline__ void quantize8(uint8_t* out, long long i, const Eight
     for (int j = 0; j < 2; ++j) {
       w[j] = 0x7F7F7F7Fu - 0x4B400000u * 0x01010101u;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[j] += b(4 * j + k) << (8 * k);
+      for (int k = 0; k < 4; ++k) w[j] += b[4 * j + k] << (8 * k);
     }
     *reinterpret_cast<uint2*>(out + i) = make_uint2(w[0], w[1]);
   }
 }
+// Whether the sum of eight values is finite (so each of them is).
+__device__ __forceinline__ u64 sum4(const Eight& x) { return add2(add2(x.v[0], x.v[1]), add2(x.v[2], x.v[3])); }
+__device__ __forceinline__ bool finite2(u64 a) { return fabsf(lo_f(a)) < INFINITY && fabsf(hi_f(a)) < INFINITY; }
 
 // A group's place in the pages and in the call.
 struct GroupAt {
@@ -373,16 +382,23 @@ __device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max
     const float sc = group_scale(m, qmax);
     s_scale[d] = sc;
     s_scale[D + d] = __frcp_rn(sc);
-    p.k_scales[head * p.k_scales_head + static_cast<long long>(in_page / g) * D + d] = sc;
+    p.k_scales[head * p.k_scales_head + static_cast<long long>(in_page >> p.lg) * D + d] = sc;
   }
   __syncthreads();
   if (!on) return;
   const Eight sc = load8f(s_scale + d0), rs = load8f(s_scale + D + d0);
+  u64 sum = sum4(x[0]);
+#pragma unroll
+  for (int q = 1; q < PASS; ++q) sum = add2(sum, sum4(x[q]));
+  bool plain = finite2(sum);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) plain = plain && plain_scale(sc.at(k));
   uint8_t* out = p.k_codes + head * p.k_codes_head;
+  const long long at = static_cast<long long>(in_page) * D + d0;
 #pragma unroll
   for (int q = 0; q < PASS; ++q) {
     const int r = q * RPP + slot;
-    if (r < g) quantize8(out, static_cast<long long>(in_page + r) * D + d0, x[q], sc, rs, p.bits);
+    if (r < g) quantize8(out, at + r * D, x[q], sc, rs, p.bits, plain);
   }
 }
 
@@ -408,24 +424,36 @@ __device__ __forceinline__ void append_v_vec(const AppendParams& p, int h, const
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) return;   // the K CTA records it
   const long long head = static_cast<long long>(page) * p.H + h;
   const int in_page = a.tok0 % p.P;
+  // a group's lanes divide its rows' scales: lane q the one of pass q
+  const int lanes = g >> 3, own = l & (lanes - 1);
+  float mx[PASS], top = 0.f;
 #pragma unroll
   for (int q = 0; q < PASS; ++q) {
-    const int r = q * RPP + slot;
     float m = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[q].at(k)));
-    for (int o = 1; o < g / 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    mx[q] = m;
+    if (q == own) top = m;
+  }
+  const float scale = group_scale(top, qmax);
+#pragma unroll
+  for (int q = 0; q < PASS; ++q) {
+    const int r = q * RPP + slot;
+    const float sc = lanes >= PASS ? __shfl_sync(0xffffffffu, scale, (threadIdx.x & 31) - own + q)
+                                   : group_scale(mx[q], qmax);
     if (on && r >= kept && r < live) {
-      const float sc = group_scale(m, qmax), rs = __frcp_rn(sc);
+      const float rs = __frcp_rn(sc);
       const long long tok = in_page + r;
-      if (d0 % g == 0) p.v_scales[head * p.v_scales_head + tok * (D / g) + d0 / g] = sc;
+      if (own == 0) p.v_scales[head * p.v_scales_head + tok * (D >> p.lg) + (d0 >> p.lg)] = sc;
       Eight s8, r8;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         s8.v[k] = pack2(sc, sc);
         r8.v[k] = pack2(rs, rs);
       }
-      quantize8(p.v_codes + head * p.v_codes_head, tok * D + d0, x[q], s8, r8, p.bits);
+      quantize8(p.v_codes + head * p.v_codes_head, tok * D + d0, x[q], s8, r8, p.bits,
+                plain_scale(sc) && finite2(sum4(x[q])));
     }
   }
 }
@@ -439,13 +467,14 @@ __global__ void __launch_bounds__(kThreads, LPR == 0 || PASS == 8 ? 3 : 6) paged
   const long long u = blockIdx.x;
   const int h = blockIdx.y, g = p.group;
   const bool v_part = blockIdx.z != 0;              // K has a CTA of its own (LPR > 0)
+  const GroupSize gs{g, LPR > 0 ? max(p.lg, 0) : p.lg};       // (the vector form's groups are powers of two)
   const int b = p.max_new == 1 ? static_cast<int>(u)
-                               : warp_find(p.S, u, [&](int i) { return unit_base(p.cu, i, p.T, g); });
+                               : warp_find(p.S, u, [&](int i) { return unit_base(p.cu, i, p.T, gs); });
   // one round of loads
   const int c0 = __ldcg(p.cu + b), len = __ldg(p.lengths + b);
   const RowRange rr = row_range(p.cu, b, p.T, p.max_new);
   const int slot = p.slots ? __ldg(p.slots + b) : b;
-  const int j = p.max_new == 1 ? 0 : static_cast<int>(u - (min(max(c0, 0), p.T) / g + 2LL * b));
+  const int j = p.max_new == 1 ? 0 : static_cast<int>(u - (gs.div(min(max(c0, 0), p.T)) + 2LL * b));
   if (j < 0) return;                                // before the first sequence's rows
   const bool report = threadIdx.x == 0 && j == 0 && h == 0 && !v_part;
   if (rr.bad && report) record_error(p.err, KVQ_ERR_LENGTH);
@@ -459,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, LPR == 0 || PASS == 8 ? 3 : 6) paged
     return;
   }
   const int first = len - rr.n;
-  const int j0 = first / g, last = (len - 1) / g - j0;
+  const int j0 = gs.div(first), last = gs.div(len - 1) - j0;
   if (j > last) return;
   const int32_t* table = p.table + static_cast<long long>(b) * p.max_pages;
   if constexpr (LPR > 0) {
@@ -469,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, LPR == 0 || PASS == 8 ? 3 : 6) paged
     }
   }
   // both ends unfinished: the CTA of the first group does the last one too
-  const bool joined = last > 0 && first % g != 0 && len % g != 0;
+  const bool joined = last > 0 && j0 * g != first && gs.div(len) * g != len;
   if (joined && j == last) return;
   float* tail = p.tail + (static_cast<long long>(slot) * p.H + h) * g * p.D;
   for (int k = j; k <= last; k += joined && j == 0 ? last : last + 1) {
@@ -672,6 +701,9 @@ kvq_status launch_append(const AppendCall& a, cudaStream_t s) {
   p.n_pos = a.rope.n_pos;
   p.rot = a.rope.table ? a.rope.rot_dim : 0;
   p.interleaved = a.rope.interleaved;
+  p.lg = -1;
+  for (int k = 0; k < 31; ++k)
+    if (a.g.group == 1 << k) p.lg = k;
   p.k_codes = a.cache->pages.k_codes;
   p.k_scales = a.cache->pages.k_scales;
   p.v_codes = a.cache->pages.v_codes;
