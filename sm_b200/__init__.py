@@ -3,7 +3,9 @@
 A thin ctypes binding over ``libkvq.so`` (the C ABI in ``include/kvq.h``).
 It only marshals arguments: torch tensors supply device pointers, the current
 CUDA stream and device memory; every step of quantize/pack and attention runs
-in the library's kernels.  If ``libkvq.so`` is missing the import fails: there
+in the library's kernels.  The paged calls marshal theirs in a small extension
+(``_calls.so``, ``csrc/torch_calls.cpp``), since a serving loop makes them once
+a layer.  If ``libkvq.so`` or ``_calls.so`` is missing the import fails: there
 is no fallback of any kind.
 
     cache = sm_b200.PackedCache(B, H_kv, N_cap, D, bits=4, group=32)
@@ -139,6 +141,11 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+try:
+    from . import _calls               # the paged calls: argument checks and tensors in C++
+except ImportError as e:
+    raise ImportError(f"_calls.so not built: run `python sm_b200/build.py` ({e})") from e
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -454,7 +461,7 @@ class PagedCache:
                                      self.v_codes.data_ptr(), self.v_scales.data_ptr()),
                               self.k_tail.data_ptr(), self.slots)
         self._ref = ctypes.byref(self._struct)
-        self._ws = {}                      # (dtype, S, T, max_q, H_q, splits) -> workspace bytes
+        self._address, self._index = ctypes.addressof(self._struct), dev.index
 
     def struct(self) -> _Paged:
         return self._struct
@@ -475,62 +482,11 @@ def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -
     return torch.cat([a.cos(), a.sin()], 1).float().contiguous()
 
 
-def _call(dev: torch.device, fn, name: str, *args) -> None:
-    """fn(*args, current stream of dev) with dev current."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    if st != 0:
-        raise KVQError(st, name)
-
-
-def _rope_arg(rope: torch.Tensor | None, interleaved: bool, D: int, dev: torch.device):
-    if rope is None:
-        return None
-    _check_cuda(rope, "rope", dev)
-    if rope.dtype != torch.float32 or rope.dim() != 2:
-        raise ValueError("rope must be float32 [n_pos, rot_dim]")
-    n_pos, rot = rope.shape
-    if rot < 2 or rot % 2 or rot > D or n_pos < 1:
-        raise ValueError("rot_dim must be even, at least 2 and at most D")
-    return _Rope(rope.data_ptr(), n_pos, rot, int(bool(interleaved)))
-
-
-def _check_rows(t: torch.Tensor, name: str, T: int, heads: int, D: int, dev: torch.device) -> int:
-    """The row stride of t [T, heads, D], whose rows may lie any distance apart."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if t.dim() != 3 or tuple(t.shape) != (T, heads, D):
-        raise ValueError(f"{name} must be [{T}, {heads}, {D}]")
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (heads > 1 and st[1] != D):
-        raise ValueError(f"{name}: the heads of a row must lie one after the other")
-    if T > 1 and st[0] < heads * D:
-        raise ValueError(f"{name}: rows must not overlap")
-    return st[0] if T > 1 else heads * D
-
-
-def _check_index(t: torch.Tensor, name: str, n: int, dev: torch.device) -> None:
-    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n:
-        raise ValueError(f"{name} must be int32 [{n}]")
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous on {dev}")
-
-
-def _check_batch(cache: PagedCache, block_table: torch.Tensor, lengths: torch.Tensor, cu: torch.Tensor,
-                 name: str = "lengths") -> int:
-    """Number of sequences of a ragged call."""
-    dev = cache.device
-    if block_table.dtype != torch.int32 or block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [S, max_pages]")
-    if block_table.device != dev or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be contiguous on {dev}")
-    S = block_table.shape[0]
-    _check_index(lengths, name, S, dev)
-    _check_index(cu, "cu", S + 1, dev)
-    return S
+def _done(r, name: str):
+    """The result of a call of the extension, or its status raised."""
+    if type(r) is int and r != 0:
+        raise KVQError(r, name)
+    return r
 
 
 def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tensor | None,
@@ -541,44 +497,8 @@ def qk_norm_rope(Q: torch.Tensor, K: torch.Tensor | None, positions: torch.Tenso
     rotation at ``positions`` (int32 [T]; rope None: none), one pass.  Q
     [T, H_q, D], K [T, H_kv, D] or None, fp32/bf16, rows any distance apart
     (views of a fused projection); returns dense (Q', K')."""
-    dev = Q.device
-    if not Q.is_cuda:
-        raise ValueError("Q must be on a CUDA device")
-    if Q.dim() != 3:
-        raise ValueError("Q must be [T, H_q, D]")
-    T, H_q, D = Q.shape
-    code = _dtype_code(Q)
-    qs = _check_rows(Q, "Q", T, H_q, D, dev)
-    H_kv, ks = 0, 0
-    if K is not None:
-        if K.dim() != 3 or K.dtype != Q.dtype:
-            raise ValueError("K must be [T, H_kv, D] of Q's dtype")
-        H_kv = K.shape[1]
-        ks = _check_rows(K, "K", T, H_kv, D, dev)
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.device != dev or w.dtype != Q.dtype or w.dim() != 1 or w.numel() != D
-                              or not w.is_contiguous()):
-            raise ValueError(f"{n} must be contiguous [D] of Q's dtype on {dev}")
-    r = _rope_arg(rope, interleaved, D, dev)
-    if r is not None:
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        _check_index(positions, "positions", T, dev)
-    if q_out is None:
-        q_out = torch.empty((T, H_q, D), dtype=Q.dtype, device=dev)
-    if k_out is None and K is not None:
-        k_out = torch.empty((T, H_kv, D), dtype=Q.dtype, device=dev)
-    for o, x, n in ((q_out, Q, "q_out"), (k_out, K, "k_out")):
-        if x is not None and (o.shape != x.shape or o.dtype != x.dtype or o.device != dev or not o.is_contiguous()):
-            raise ValueError(f"{n} must be contiguous and match its input")
-    if T == 0:
-        return q_out, k_out
-    _call(dev, lib.kvq_qk_norm_rope, "kvq_qk_norm_rope", Q.data_ptr(), qs, K.data_ptr() if K is not None else None, ks,
-          code, T, H_q, H_kv, D, q_weight.data_ptr() if q_weight is not None else None,
-          k_weight.data_ptr() if k_weight is not None else None, float(eps),
-          positions.data_ptr() if r is not None else None, ctypes.byref(r) if r is not None else None,
-          q_out.data_ptr(), k_out.data_ptr() if K is not None else None)
-    return q_out, k_out
+    return _done(_calls.qk_norm_rope(Q, K, positions, rope, q_weight, k_weight, eps, interleaved, q_out, k_out),
+                 "kvq_qk_norm_rope")
 
 
 def paged_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, block_table: torch.Tensor,
@@ -589,23 +509,8 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, block_tabl
     tokens lengths[b] - n .. lengths[b] - 1 (lengths count them), K rotated by
     its position on the way if ``rope`` is given.  ``slots`` int32 [S]: each
     sequence's row of ``cache.k_tail`` (default: b)."""
-    dev, H, D = cache.device, cache.H_kv, cache.D
-    S = _check_batch(cache, block_table, lengths, cu)
-    if K.dim() != 3 or K.dtype != V.dtype:
-        raise ValueError("K and V must be [T, H_kv, D] of one dtype")
-    T = K.shape[0]
-    ks, vs = _check_rows(K, "K", T, H, D, dev), _check_rows(V, "V", T, H, D, dev)
-    if slots is not None:
-        _check_index(slots, "slots", S, dev)
-    elif S > cache.slots:
-        raise ValueError("more sequences than the cache has tail slots")
-    r = _rope_arg(rope, interleaved, D, dev)
-    if T == 0 or S == 0:
-        return
-    _call(dev, lib.kvq_paged_append, "kvq_paged_append", cache._ref, K.data_ptr(), ks, V.data_ptr(), vs, _dtype_code(K),
-          block_table.data_ptr(), block_table.shape[1], lengths.data_ptr(), cu.data_ptr(),
-          slots.data_ptr() if slots is not None else None, S, T, int(max_new),
-          ctypes.byref(r) if r is not None else None)
+    _done(_calls.paged_append(cache._address, cache._index, K, V, block_table, lengths, cu, max_new, rope, interleaved,
+                              slots), "kvq_paged_append")
 
 
 def paged_gather(cache: PagedCache, block_table: torch.Tensor, starts: torch.Tensor, cu: torch.Tensor, rows: int,
@@ -613,28 +518,17 @@ def paged_gather(cache: PagedCache, block_table: torch.Tensor, starts: torch.Ten
     """Tokens [starts[b], starts[b] + cu[b + 1] - cu[b]) of each sequence as
     the values their codes stand for: dense K, V [rows, H_kv, D], rows
     [cu[b], cu[b + 1]) of them (others are left unwritten)."""
-    dev = cache.device
-    S = _check_batch(cache, block_table, starts, cu, "starts")
-    K = torch.empty((rows, cache.H_kv, cache.D), dtype=dtype, device=dev)
-    V = torch.empty_like(K)
-    code = _dtype_code(K)
-    if rows > 0 and S > 0:
-        _call(dev, lib.kvq_paged_gather, "kvq_paged_gather", cache._ref, block_table.data_ptr(), block_table.shape[1],
-              starts.data_ptr(), cu.data_ptr(), S, rows, int(max_rows), K.data_ptr(), V.data_ptr(), code)
-    return K, V
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"unsupported dtype {dtype}: float32 or bfloat16")
+    return _done(_calls.paged_gather(cache._address, cache._index, block_table, starts, cu, rows, max_rows,
+                                     dtype is torch.bfloat16), "kvq_paged_gather")
 
 
 def paged_workspace_size(cache: PagedCache, dtype: torch.dtype, S: int, T: int, max_q: int, H_q: int,
                          splits: int = 0) -> int:
-    key = (dtype, S, T, max_q, H_q, splits)
-    n = cache._ws.get(key)
-    if n is None:
-        n = int(lib.kvq_paged_workspace_size(cache._ref, KVQ_F32 if dtype == torch.float32 else KVQ_BF16, S, T, max_q,
-                                             H_q, splits))
-        if len(cache._ws) > 4096:          # ragged batches: T changes from call to call
-            cache._ws.clear()
-        cache._ws[key] = n
-    return n
+    """Bytes of workspace paged_attend needs for these sizes (0: not valid)."""
+    return int(lib.kvq_paged_workspace_size(cache._ref, KVQ_F32 if dtype == torch.float32 else KVQ_BF16, S, T, max_q,
+                                            H_q, splits))
 
 
 def paged_kernel_name(cache: PagedCache, dtype: torch.dtype, max_q: int, H_q: int) -> str:
@@ -650,30 +544,8 @@ def paged_attend(Q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, 
     it reads the keys up to its own position, else all lengths[b] keys.
     ``max_q``: upper bound of the rows a sequence has.  Returns O like Q; rows
     from cu[S] on are left as they were."""
-    dev = cache.device
-    S = _check_batch(cache, block_table, lengths, cu)
-    _check_cuda(Q, "Q", dev)
-    if Q.dim() != 3 or Q.shape[2] != cache.D:
-        raise ValueError("Q must be [T, H_q, D]")
-    T, H_q, _ = Q.shape
-    code = _dtype_code(Q)
-    if out is None:
-        out = torch.empty_like(Q)
-    else:
-        _check_cuda(out, "out", dev)
-        if out.shape != Q.shape or out.dtype != Q.dtype:
-            raise ValueError("out must match Q")
-    if T == 0 or S == 0:
-        return out
-    need = paged_workspace_size(cache, Q.dtype, S, T, int(max_q), H_q, int(splits))
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    else:
-        _check_cuda(workspace, "workspace", dev)
-    _call(dev, lib.kvq_paged_attend, "kvq_paged_attend", Q.data_ptr(), code, cache._ref, block_table.data_ptr(),
-          block_table.shape[1], lengths.data_ptr(), cu.data_ptr(), S, T, int(max_q), H_q, float(scale), int(bool(causal)),
-          out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(splits))
-    return out
+    return _done(_calls.paged_attend(cache._address, cache._index, Q, block_table, lengths, cu, max_q, scale, causal, out,
+                                     workspace, splits), "kvq_paged_attend")
 
 
 def check(device=None) -> None:

@@ -1,10 +1,13 @@
-"""Build libkvq.so in-tree for sm_100a with nvcc.
+"""Build libkvq.so in-tree for sm_100a with nvcc, and _calls.so against torch.
 
     python sm_b200/build.py [--force] [--verbose]
 
 Every ``csrc/*.cu`` file compiles to an object under ``_build/`` (in
-parallel), and the objects link into ``sm_b200/libkvq.so``.  A source or
-header newer than the library triggers a rebuild.
+parallel), and the objects link into ``sm_b200/libkvq.so``;
+``csrc/torch_calls.cpp`` (the paged calls of the Python binding) compiles with
+the host compiler against torch's headers and libkvq.so into
+``sm_b200/_calls.so``.  A source or header newer than its library triggers a
+rebuild.
 """
 
 from __future__ import annotations
@@ -22,6 +25,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
+CALLS = os.path.join(HERE, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
@@ -63,8 +68,31 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_calls(force: bool = False) -> str:
+    deps = [CALLS_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(ROOT, "include", "*.h"))]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+        return CALLS
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for p in inc for a in ("-isystem", p)], CALLS_SRC, "-o", tmp, "-L", HERE, "-l:libkvq.so",
+           "-L", os.path.join(base, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {CALLS_SRC}:\n{res.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_calls(force)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
@@ -75,6 +103,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    build_calls(force)
     return LIB
 
 

@@ -129,6 +129,10 @@ def test_binding_refuses_on_the_host():
         K.rope_table(16, 7, device=cpu)
     with pytest.raises(ValueError):
         K.qk_norm_rope(torch.zeros(2, 4, 64), None, None, None)     # not on a GPU
+    with pytest.raises(TypeError):
+        K.qk_norm_rope(3, None, None, None)
+    with pytest.raises(TypeError):
+        K._calls.paged_append(1)
     with pytest.raises(ValueError):                                 # given buffers must be on the cache's GPU
         K.PagedCache(4, 2, 64, 64, device=cpu, buffers=[torch.zeros(1, dtype=torch.uint8)] * 5)
 
