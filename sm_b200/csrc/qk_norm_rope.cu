@@ -27,7 +27,7 @@ struct Params {
   int n_pos, rot, interleaved;
   void* Q_out;
   void* K_out;
-  int rows_per_warp;
+  float inv_d;
   unsigned int* err;
 };
 
@@ -44,9 +44,11 @@ struct Vec;                                    // 16 bytes of T
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void load(const void* p, long long i, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  static __device__ __forceinline__ uint4 load(const void* p, long long i) {
+    return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+  }
+  static __device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   }
   static __device__ __forceinline__ void store(void* p, long long i, const float (&x)[4]) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
@@ -55,8 +57,10 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void load(const void* p, long long i, float (&x)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+  static __device__ __forceinline__ uint4 load(const void* p, long long i) {
+    return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+  }
+  static __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
     const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -76,21 +80,31 @@ struct Vec<__nv_bfloat16> {
 };
 
 // Vector path: LPR lanes hold a row (a power of two; D = LPR * N); the pairs
-// of the rotation lie within a lane (interleaved) or whole lanes apart.
-template <typename T, int LPR>
+// of the rotation lie within a lane (interleaved) or whole lanes apart.  A
+// warp takes U * 32 / LPR heads of one token: all their loads go out before
+// the position's and the table's answer comes back.
+template <typename T, int LPR, int U>
 __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
   griddep_wait();
-  constexpr int N = Vec<T>::N, RPW = 32 / LPR;   // rows a warp holds at once
+  constexpr int N = Vec<T>::N, RPW = 32 / LPR, HEADS = RPW * U;   // rows a warp loads at once; its heads
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-  const int heads = p.H_q + (p.K ? p.H_kv : 0);
-  const int per_token = (heads + p.rows_per_warp - 1) / p.rows_per_warp;
+  const int heads = p.H_q + p.H_kv;
+  const int per_token = (heads + HEADS - 1) / HEADS;
   const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
   if (unit >= static_cast<long long>(p.T) * per_token) return;
-  const int t = static_cast<int>(unit / per_token), h0 = static_cast<int>(unit % per_token) * p.rows_per_warp;
-  const int h1 = min(heads, h0 + p.rows_per_warp);
-  const int pos = rope_position(p, t, lane == 0 && h0 == 0);
+  const int t = static_cast<int>(unit / per_token), h0 = static_cast<int>(unit - static_cast<long long>(t) * per_token) * HEADS;
   const int half = p.rot / 2, d0 = l * N;
-  // this lane's angles: interleaved, N / 2 pairs; else one pair element per feature
+  uint4 raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * RPW + sub;
+    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < heads)
+      raw[u] = h < p.H_q ? Vec<T>::load(p.Q, t * p.q_stride + static_cast<long long>(h) * p.D + d0)
+                         : Vec<T>::load(p.K, t * p.k_stride + static_cast<long long>(h - p.H_q) * p.D + d0);
+  }
+  const int pos = rope_position(p, t, lane == 0 && h0 == 0);
+  // this lane's angles; the sign of s makes both features of a pair x c + partner s
   float c[N], s[N];
   int partner = lane;
   const bool turns = pos >= 0 && d0 < p.rot;
@@ -125,50 +139,36 @@ __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
       }
     }
   }
-  for (int h = h0; h < h1; h += RPW) {
-    const int hh = h + sub;
-    const bool on = hh < h1, is_k = hh >= p.H_q;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * RPW + sub;
+    const bool on = h < heads, is_k = h >= p.H_q;
     float x[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = 0.f;
-    if (on) {
-      if (is_k) Vec<T>::load(p.K, t * p.k_stride + static_cast<long long>(hh - p.H_q) * p.D + d0, x);
-      else Vec<T>::load(p.Q, t * p.q_stride + static_cast<long long>(hh) * p.D + d0, x);
-    }
+    Vec<T>::widen(raw[u], x);
     const void* w = is_k ? p.k_weight : p.q_weight;
-    float sum = 0.f;
+    if (p.k_weight || p.q_weight) {
+      float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) sum = fmaf(x[k], x[k], sum);
+      for (int k = 0; k < N; ++k) sum = fmaf(x[k], x[k], sum);
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (on && w) {
-      float wv[N];
-      Vec<T>::load(w, d0, wv);
-      const float r = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+      for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (on && w) {
+        float wv[N];
+        Vec<T>::widen(Vec<T>::load(w, d0), wv);
+        const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = x[k] * r * wv[k];
+        for (int k = 0; k < N; ++k) x[k] = x[k] * r * wv[k];
+      }
     }
     float y[N];
-    if (p.interleaved) {
 #pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        y[k] = fmaf(x[k + 1], s[k], x[k] * c[k]);
-        y[k + 1] = fmaf(x[k], s[k + 1], x[k + 1] * c[k + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const float o = __shfl_sync(0xffffffffu, x[k], partner);
-        y[k] = fmaf(o, s[k], x[k] * c[k]);
-      }
-    }
-    if (!turns) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) y[k] = x[k];
+    for (int k = 0; k < N; ++k) {
+      const float o = p.interleaved ? x[k ^ 1] : __shfl_sync(0xffffffffu, x[k], partner);
+      y[k] = turns ? fmaf(o, s[k], x[k] * c[k]) : x[k];
     }
     if (on) {
-      if (is_k) Vec<T>::store(p.K_out, (static_cast<long long>(t) * p.H_kv + hh - p.H_q) * p.D + d0, y);
-      else Vec<T>::store(p.Q_out, (static_cast<long long>(t) * p.H_q + hh) * p.D + d0, y);
+      if (is_k) Vec<T>::store(p.K_out, (static_cast<long long>(t) * p.H_kv + h - p.H_q) * p.D + d0, y);
+      else Vec<T>::store(p.Q_out, (static_cast<long long>(t) * p.H_q + h) * p.D + d0, y);
     }
   }
 }
@@ -237,24 +237,25 @@ kvq_status launch(Params p, cudaStream_t s) {
                    (p.rot == 0 || (p.interleaved ? p.rot % N == 0
                                                  : p.rot % (2 * N) == 0 && aligned16(p.rope)));
   if (vec) {
-    // heads a warp takes one after the other: enough to use its angles more
-    // than once, while the warps still fill the GPU
+    // four loads a warp in flight where that leaves enough warps to fill the GPU
+    // (148 SMs of 32 warps), one where it would not: at 64 tokens of 40 heads
+    // the step is latency, and fewer heads a warp finish sooner
     const int rpw = 32 / lpr;
-    int rows = rpw;
-    while (rows < heads && static_cast<long long>(p.T) * ((heads + rows - 1) / rows) > 148 * 64) rows += rpw;
-    p.rows_per_warp = rows;
+    const bool many = static_cast<long long>(p.T) * ((heads + 4 * rpw - 1) / (4 * rpw)) >= 148 * 32;
+    const int rows = many ? 4 * rpw : rpw;
     const long long units = static_cast<long long>(p.T) * ((heads + rows - 1) / rows);
     const long long grid = (units + warps - 1) / warps;
     if (grid > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
     cudaError_t e = cudaErrorInvalidValue;
     const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
+    auto run = [&](auto one, auto four) { e = many ? launch_pdl(four, g, b, 0, s, p) : launch_pdl(one, g, b, 0, s, p); };
     switch (lpr) {
-      case 1: e = launch_pdl(qk_vec_kernel<T, 1>, g, b, 0, s, p); break;
-      case 2: e = launch_pdl(qk_vec_kernel<T, 2>, g, b, 0, s, p); break;
-      case 4: e = launch_pdl(qk_vec_kernel<T, 4>, g, b, 0, s, p); break;
-      case 8: e = launch_pdl(qk_vec_kernel<T, 8>, g, b, 0, s, p); break;
-      case 16: e = launch_pdl(qk_vec_kernel<T, 16>, g, b, 0, s, p); break;
-      case 32: e = launch_pdl(qk_vec_kernel<T, 32>, g, b, 0, s, p); break;
+      case 1: run(qk_vec_kernel<T, 1, 1>, qk_vec_kernel<T, 1, 4>); break;
+      case 2: run(qk_vec_kernel<T, 2, 1>, qk_vec_kernel<T, 2, 4>); break;
+      case 4: run(qk_vec_kernel<T, 4, 1>, qk_vec_kernel<T, 4, 4>); break;
+      case 8: run(qk_vec_kernel<T, 8, 1>, qk_vec_kernel<T, 8, 4>); break;
+      case 16: run(qk_vec_kernel<T, 16, 1>, qk_vec_kernel<T, 16, 4>); break;
+      case 32: run(qk_vec_kernel<T, 32, 1>, qk_vec_kernel<T, 32, 4>); break;
     }
     if (e != cudaSuccess) return KVQ_ERR_CUDA;
   } else {
@@ -306,6 +307,7 @@ extern "C" kvq_status kvq_qk_norm_rope(const void* Q, int64_t q_stride, const vo
   p.q_weight = q_weight;
   p.k_weight = k_weight;
   p.eps = eps;
+  p.inv_d = 1.f / static_cast<float>(D);
   p.positions = positions;
   p.rope = turn ? rope->table : nullptr;
   p.n_pos = turn ? rope->n_pos : 0;
