@@ -7,6 +7,7 @@
 // features is held by a few lanes, 16 bytes each, so one load brings a row's
 // part, shuffles give the sum of squares and (pairs D/2 apart) the partner,
 // and a warp takes several heads of one token, whose angles it loads once.
+#include "f32x2.cuh"
 #include "kvq_internal.cuh"
 
 namespace kvq {
@@ -39,137 +40,156 @@ __device__ __forceinline__ int rope_position(const Params& p, int t, bool report
   return -1;
 }
 
+// 16 bytes of T as pairs of floats.
 template <typename T>
-struct Vec;                                    // 16 bytes of T
+struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ uint4 load(const void* p, long long i) {
-    return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+  static __device__ __forceinline__ void widen(const uint4& v, u64 (&x)[2]) {
+    x[0] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
   }
-  static __device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
-    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
-  }
-  static __device__ __forceinline__ void store(void* p, long long i, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
+  // the features of each pair exchanged
+  static __device__ __forceinline__ uint4 exchange(const uint4& v) { return make_uint4(v.y, v.x, v.w, v.z); }
+  static __device__ __forceinline__ void store(void* p, long long i, const u64 (&x)[2]) {
+    *reinterpret_cast<ulonglong2*>(static_cast<float*>(p) + i) = make_ulonglong2(x[0], x[1]);
   }
 };
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ uint4 load(const void* p, long long i) {
-    return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-  }
-  static __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
+  static __device__ __forceinline__ void widen(const uint4& v, u64 (&x)[4]) {
     const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
+    for (int k = 0; k < 4; ++k) x[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void store(void* p, long long i, const float (&x)[8]) {
+  static __device__ __forceinline__ uint4 exchange(const uint4& v) {
+    return make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032), __byte_perm(v.z, 0, 0x1032),
+                      __byte_perm(v.w, 0, 0x1032));
+  }
+  static __device__ __forceinline__ void store(void* p, long long i, const u64 (&x)[4]) {
     unsigned w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(lo_f(x[k]), hi_f(x[k]));
       w[k] = *reinterpret_cast<const unsigned*>(&b);
     }
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
+template <typename T>
+__device__ __forceinline__ uint4 load16(const void* p, long long i) {
+  return *reinterpret_cast<const uint4*>(static_cast<const T*>(p) + i);
+}
 
 // Vector path: LPR lanes hold a row (a power of two; D = LPR * N); the pairs
 // of the rotation lie within a lane (interleaved) or whole lanes apart.  A
-// warp takes U * 32 / LPR heads of one token: all their loads go out before
-// the position's and the table's answer comes back.
+// warp takes U * 32 / LPR heads of one token, all of Q or all of K: their
+// loads go out before the position's and the table's answers come back, and
+// weight times angle is formed once for all of them, so that a feature costs
+// y = r (x wc + partner ws): two products and a fused sum, on pairs.
 template <typename T, int LPR, int U>
 __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
   griddep_wait();
   constexpr int N = Vec<T>::N, RPW = 32 / LPR, HEADS = RPW * U;   // rows a warp loads at once; its heads
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-  const int heads = p.H_q + p.H_kv;
-  const int per_token = (heads + HEADS - 1) / HEADS;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(p.T) * per_token) return;
-  const int t = static_cast<int>(unit / per_token), h0 = static_cast<int>(unit - static_cast<long long>(t) * per_token) * HEADS;
+  const int q_units = (p.H_q + HEADS - 1) / HEADS, per_token = q_units + (p.H_kv + HEADS - 1) / HEADS;
+  const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int t = static_cast<int>(unit / per_token), part = static_cast<int>(unit - static_cast<unsigned>(t) * per_token);
+  if (t >= p.T) return;
+  const bool is_k = part >= q_units;
+  const int heads = is_k ? p.H_kv : p.H_q, h0 = (is_k ? part - q_units : part) * HEADS + sub;
   const int half = p.rot / 2, d0 = l * N;
+  const T* src = static_cast<const T*>(is_k ? p.K : p.Q) + t * (is_k ? p.k_stride : p.q_stride) + h0 * p.D + d0;
+  T* dst = static_cast<T*>(is_k ? p.K_out : p.Q_out) + (static_cast<long long>(t) * heads + h0) * p.D + d0;
   uint4 raw[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RPW + sub;
-    raw[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < heads)
-      raw[u] = h < p.H_q ? Vec<T>::load(p.Q, t * p.q_stride + static_cast<long long>(h) * p.D + d0)
-                         : Vec<T>::load(p.K, t * p.k_stride + static_cast<long long>(h - p.H_q) * p.D + d0);
-  }
-  const int pos = rope_position(p, t, lane == 0 && h0 == 0);
-  // this lane's angles; the sign of s makes both features of a pair x c + partner s
-  float c[N], s[N];
-  int partner = lane;
+  for (int u = 0; u < U; ++u)
+    raw[u] = h0 + u * RPW < heads ? load16<T>(src, u * RPW * p.D) : make_uint4(0u, 0u, 0u, 0u);
+  const int pos = rope_position(p, t, lane == 0 && part == 0);
   const bool turns = pos >= 0 && d0 < p.rot;
+  const bool upper = !p.interleaved && d0 >= half;
+  const int shift = turns && !p.interleaved ? (upper ? -half / N : half / N) : 0;   // the partner lane's distance
+  // wc = w c and ws = (partner's w) (+-s) of this lane's features
+  u64 wc[N / 2], ws[N / 2];
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    c[k] = 1.f;
-    s[k] = 0.f;
+  for (int k = 0; k < N / 2; ++k) {
+    wc[k] = pack2(1.f, 1.f);
+    ws[k] = 0ull;
   }
   if (turns) {
     const float* tab = p.rope + static_cast<long long>(pos) * p.rot;
     if (p.interleaved) {
 #pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        c[k] = c[k + 1] = __ldg(tab + d0 / 2 + k / 2);
-        s[k + 1] = __ldg(tab + half + d0 / 2 + k / 2);
-        s[k] = -s[k + 1];
+      for (int k = 0; k < N / 2; ++k) {
+        const float c = __ldg(tab + d0 / 2 + k), s = __ldg(tab + half + d0 / 2 + k);
+        wc[k] = pack2(c, c);
+        ws[k] = pack2(-s, s);
       }
     } else {
-      const bool upper = d0 >= half;
       const int e = upper ? d0 - half : d0;
-      partner = upper ? lane - half / N : lane + half / N;
+      const u64 flip = upper ? 0ull : 0x8000000080000000ull;
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(tab + e + k));
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(tab + half + e + k));
-        c[k] = cv.x; c[k + 1] = cv.y; c[k + 2] = cv.z; c[k + 3] = cv.w;
-        s[k] = sv.x; s[k + 1] = sv.y; s[k + 2] = sv.z; s[k + 3] = sv.w;
-      }
-      if (!upper) {
-#pragma unroll
-        for (int k = 0; k < N; ++k) s[k] = -s[k];
+      for (int k = 0; k < N / 2; k += 2) {
+        const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(tab + e + 2 * k);
+        const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(tab + half + e + 2 * k);
+        wc[k] = c.x;
+        wc[k + 1] = c.y;
+        ws[k] = s.x ^ flip;
+        ws[k + 1] = s.y ^ flip;
       }
     }
   }
+  const void* w = is_k ? p.k_weight : p.q_weight;
+  if (w) {
+    const uint4 own = load16<T>(w, d0), other = p.interleaved ? Vec<T>::exchange(own) : load16<T>(w, d0 + shift * N);
+    u64 wv[N / 2];
+    Vec<T>::widen(own, wv);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) wc[k] = mul2(wc[k], wv[k]);
+    Vec<T>::widen(other, wv);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) ws[k] = mul2(ws[k], wv[k]);
+  }
+  const unsigned mask = turns ? 0xFFFFFFFFu : 0u;      // a lane that does not turn has no partner: inf * 0 stays out
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int h = h0 + u * RPW + sub;
-    const bool on = h < heads, is_k = h >= p.H_q;
-    float x[N];
+    u64 x[N / 2], o[N / 2], y[N / 2];
     Vec<T>::widen(raw[u], x);
-    const void* w = is_k ? p.k_weight : p.q_weight;
-    if (p.k_weight || p.q_weight) {
-      float sum = 0.f;
+    u64 r2 = pack2(1.f, 1.f);
+    if (w) {
+      u64 sq = mul2(x[0], x[0]);
 #pragma unroll
-      for (int k = 0; k < N; ++k) sum = fmaf(x[k], x[k], sum);
+      for (int k = 1; k < N / 2; ++k) sq = fma2(x[k], x[k], sq);
+      float sum = lo_f(sq) + hi_f(sq);
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (on && w) {
-        float wv[N];
-        Vec<T>::widen(Vec<T>::load(w, d0), wv);
-        const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = x[k] * r * wv[k];
+      for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+      r2 = pack2(r, r);
+    }
+    if (p.rot > 0) {
+      uint4 b;
+      if (p.interleaved) {
+        b = Vec<T>::exchange(raw[u]);
+      } else {
+        b.x = __shfl_sync(0xffffffffu, raw[u].x, lane + shift);
+        b.y = __shfl_sync(0xffffffffu, raw[u].y, lane + shift);
+        b.z = __shfl_sync(0xffffffffu, raw[u].z, lane + shift);
+        b.w = __shfl_sync(0xffffffffu, raw[u].w, lane + shift);
       }
-    }
-    float y[N];
+      Vec<T>::widen(make_uint4(b.x & mask, b.y & mask, b.z & mask, b.w & mask), o);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const float o = p.interleaved ? x[k ^ 1] : __shfl_sync(0xffffffffu, x[k], partner);
-      y[k] = turns ? fmaf(o, s[k], x[k] * c[k]) : x[k];
+      for (int k = 0; k < N / 2; ++k) y[k] = fma2(o[k], ws[k], mul2(x[k], wc[k]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) y[k] = mul2(x[k], wc[k]);
     }
-    if (on) {
-      if (is_k) Vec<T>::store(p.K_out, (static_cast<long long>(t) * p.H_kv + h - p.H_q) * p.D + d0, y);
-      else Vec<T>::store(p.Q_out, (static_cast<long long>(t) * p.H_q + h) * p.D + d0, y);
+    if (w) {
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) y[k] = mul2(y[k], r2);
     }
+    if (h0 + u * RPW < heads) Vec<T>::store(dst, u * RPW * p.D, y);
   }
 }
 
@@ -241,11 +261,12 @@ kvq_status launch(Params p, cudaStream_t s) {
     // (148 SMs of 32 warps), one where it would not: at 64 tokens of 40 heads
     // the step is latency, and fewer heads a warp finish sooner
     const int rpw = 32 / lpr;
-    const bool many = static_cast<long long>(p.T) * ((heads + 4 * rpw - 1) / (4 * rpw)) >= 148 * 32;
-    const int rows = many ? 4 * rpw : rpw;
-    const long long units = static_cast<long long>(p.T) * ((heads + rows - 1) / rows);
-    const long long grid = (units + warps - 1) / warps;
-    if (grid > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+    auto units_of = [&](int rows) {
+      return static_cast<long long>(p.T) * ((p.H_q + rows - 1) / rows + (p.H_kv + rows - 1) / rows);
+    };
+    const bool many = units_of(4 * rpw) >= 148 * 32;
+    const long long grid = (units_of(many ? 4 * rpw : rpw) + warps - 1) / warps;
+    if (grid > 0x3fffffffLL) return KVQ_ERR_UNSUPPORTED;
     cudaError_t e = cudaErrorInvalidValue;
     const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
     auto run = [&](auto one, auto four) { e = many ? launch_pdl(four, g, b, 0, s, p) : launch_pdl(one, g, b, 0, s, p); };
