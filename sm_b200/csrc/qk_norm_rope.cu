@@ -7,6 +7,8 @@
 // features is held by a few lanes, 16 bytes each, so one load brings a row's
 // part, shuffles give the sum of squares and (pairs D/2 apart) the partner,
 // and a warp takes several heads of one token, whose angles it loads once.
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "kvq_internal.cuh"
 
@@ -29,6 +31,7 @@ struct Params {
   void* Q_out;
   void* K_out;
   float inv_d;
+  int chunks;                    // vector path: chunks of a token that a warp takes
   unsigned int* err;
 };
 
@@ -84,48 +87,56 @@ __device__ __forceinline__ uint4 load16(const void* p, long long i) {
 }
 
 // Vector path: LPR lanes hold a row (a power of two; D = LPR * N); the pairs
-// of the rotation lie within a lane (interleaved) or whole lanes apart.  A
-// warp takes U * 32 / LPR heads of one token, all of Q or all of K: their
-// loads go out before the position's and the table's answers come back, and
-// weight times angle is formed once for all of them, so that a feature costs
-// y = r (x wc + partner ws): two products and a fused sum, on pairs.
-template <typename T, int LPR, int U>
+// of the rotation lie within a lane (kInter) or whole lanes apart.  A chunk is
+// U * 32 / LPR heads of one token, all of Q or all of K; a warp takes
+// p.chunks of a token's chunks one after the other, the next one's loads in
+// flight while it works.  Weight times angle is formed once a token and side,
+// so a feature costs y = r (x wc + partner ws): two products and a fused sum,
+// on pairs.
+template <typename T, int LPR, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
   griddep_wait();
-  constexpr int N = Vec<T>::N, RPW = 32 / LPR, HEADS = RPW * U;   // rows a warp loads at once; its heads
+  constexpr int N = Vec<T>::N, RPW = 32 / LPR, HEADS = RPW * U;   // rows a warp loads at once; a chunk's heads
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-  const int q_units = (p.H_q + HEADS - 1) / HEADS, per_token = q_units + (p.H_kv + HEADS - 1) / HEADS;
+  const int q_chunks = (p.H_q + HEADS - 1) / HEADS, chunks = q_chunks + (p.H_kv + HEADS - 1) / HEADS;
+  const int per_token = (chunks + p.chunks - 1) / p.chunks;
   const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int t = static_cast<int>(unit / per_token), part = static_cast<int>(unit - static_cast<unsigned>(t) * per_token);
+  const int t = static_cast<int>(unit / per_token);
   if (t >= p.T) return;
-  const bool is_k = part >= q_units;
-  const int heads = is_k ? p.H_kv : p.H_q, h0 = (is_k ? part - q_units : part) * HEADS + sub;
+  int ch = static_cast<int>(unit - static_cast<unsigned>(t) * per_token) * p.chunks;
+  const int ch_end = min(chunks, ch + p.chunks);
   const int half = p.rot / 2, d0 = l * N;
-  const T* src = static_cast<const T*>(is_k ? p.K : p.Q) + t * (is_k ? p.k_stride : p.q_stride) + h0 * p.D + d0;
-  T* dst = static_cast<T*>(is_k ? p.K_out : p.Q_out) + (static_cast<long long>(t) * heads + h0) * p.D + d0;
-  uint4 raw[U];
+  const T* q_row = static_cast<const T*>(p.Q) + t * p.q_stride + sub * p.D + d0;
+  const T* k_row = static_cast<const T*>(p.K) + t * p.k_stride + sub * p.D + d0;
+  auto load = [&](int c, uint4 (&raw)[U]) {
+    const bool is_k = c >= q_chunks;
+    const int h = (is_k ? c - q_chunks : c) * HEADS, left = (is_k ? p.H_kv : p.H_q) - h - sub;
+    const T* src = (is_k ? k_row : q_row) + h * p.D;
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    raw[u] = h0 + u * RPW < heads ? load16<T>(src, u * RPW * p.D) : make_uint4(0u, 0u, 0u, 0u);
-  const int pos = rope_position(p, t, lane == 0 && part == 0);
+    for (int u = 0; u < U; ++u)
+      raw[u] = u * RPW < left ? load16<T>(src, u * RPW * p.D) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 raw[U];
+  load(ch, raw);
+  const int pos = rope_position(p, t, lane == 0 && ch == 0);
   const bool turns = pos >= 0 && d0 < p.rot;
-  const bool upper = !p.interleaved && d0 >= half;
-  const int shift = turns && !p.interleaved ? (upper ? -half / N : half / N) : 0;   // the partner lane's distance
-  // wc = w c and ws = (partner's w) (+-s) of this lane's features
-  u64 wc[N / 2], ws[N / 2];
+  const bool upper = !kInter && d0 >= half;
+  const int shift = turns && !kInter ? (upper ? -half / N : half / N) : 0;   // the partner lane's distance
+  // the angles; the sign of s makes both features of a pair x c + partner s
+  u64 c2[N / 2], s2[N / 2];
 #pragma unroll
   for (int k = 0; k < N / 2; ++k) {
-    wc[k] = pack2(1.f, 1.f);
-    ws[k] = 0ull;
+    c2[k] = pack2(1.f, 1.f);
+    s2[k] = 0ull;
   }
   if (turns) {
     const float* tab = p.rope + static_cast<long long>(pos) * p.rot;
-    if (p.interleaved) {
+    if (kInter) {
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) {
         const float c = __ldg(tab + d0 / 2 + k), s = __ldg(tab + half + d0 / 2 + k);
-        wc[k] = pack2(c, c);
-        ws[k] = pack2(-s, s);
+        c2[k] = pack2(c, c);
+        s2[k] = pack2(-s, s);
       }
     } else {
       const int e = upper ? d0 - half : d0;
@@ -134,43 +145,48 @@ __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
       for (int k = 0; k < N / 2; k += 2) {
         const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(tab + e + 2 * k);
         const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(tab + half + e + 2 * k);
-        wc[k] = c.x;
-        wc[k + 1] = c.y;
-        ws[k] = s.x ^ flip;
-        ws[k + 1] = s.y ^ flip;
+        c2[k] = c.x;
+        c2[k + 1] = c.y;
+        s2[k] = s.x ^ flip;
+        s2[k + 1] = s.y ^ flip;
       }
     }
   }
-  const void* w = is_k ? p.k_weight : p.q_weight;
-  if (w) {
-    const uint4 own = load16<T>(w, d0), other = p.interleaved ? Vec<T>::exchange(own) : load16<T>(w, d0 + shift * N);
-    u64 wv[N / 2];
-    Vec<T>::widen(own, wv);
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) wc[k] = mul2(wc[k], wv[k]);
-    Vec<T>::widen(other, wv);
-#pragma unroll
-    for (int k = 0; k < N / 2; ++k) ws[k] = mul2(ws[k], wv[k]);
-  }
   const unsigned mask = turns ? 0xFFFFFFFFu : 0u;      // a lane that does not turn has no partner: inf * 0 stays out
+  u64 wc[N / 2], ws[N / 2];
+  const void* w = nullptr;
+  int side = -1;
+  for (; ch < ch_end; ++ch) {
+    const bool is_k = ch >= q_chunks;
+    if (side != static_cast<int>(is_k)) {
+      side = is_k;
+      w = is_k ? p.k_weight : p.q_weight;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    u64 x[N / 2], o[N / 2], y[N / 2];
-    Vec<T>::widen(raw[u], x);
-    u64 r2 = pack2(1.f, 1.f);
-    if (w) {
-      u64 sq = mul2(x[0], x[0]);
+      for (int k = 0; k < N / 2; ++k) {
+        wc[k] = c2[k];
+        ws[k] = s2[k];
+      }
+      if (w) {
+        const uint4 own = load16<T>(w, d0), other = kInter ? Vec<T>::exchange(own) : load16<T>(w, d0 + shift * N);
+        u64 wv[N / 2];
+        Vec<T>::widen(own, wv);
 #pragma unroll
-      for (int k = 1; k < N / 2; ++k) sq = fma2(x[k], x[k], sq);
-      float sum = lo_f(sq) + hi_f(sq);
+        for (int k = 0; k < N / 2; ++k) wc[k] = mul2(wc[k], wv[k]);
+        Vec<T>::widen(other, wv);
 #pragma unroll
-      for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
-      r2 = pack2(r, r);
+        for (int k = 0; k < N / 2; ++k) ws[k] = mul2(ws[k], wv[k]);
+      }
     }
-    if (p.rot > 0) {
+    uint4 next[U];
+    if (ch + 1 < ch_end) load(ch + 1, next);
+    const int h = (is_k ? ch - q_chunks : ch) * HEADS + sub, heads = is_k ? p.H_kv : p.H_q;
+    T* dst = static_cast<T*>(is_k ? p.K_out : p.Q_out) + (static_cast<long long>(t) * heads + h) * p.D + d0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      u64 x[N / 2], o[N / 2], y[N / 2];
+      Vec<T>::widen(raw[u], x);
       uint4 b;
-      if (p.interleaved) {
+      if (kInter) {
         b = Vec<T>::exchange(raw[u]);
       } else {
         b.x = __shfl_sync(0xffffffffu, raw[u].x, lane + shift);
@@ -181,15 +197,22 @@ __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
       Vec<T>::widen(make_uint4(b.x & mask, b.y & mask, b.z & mask, b.w & mask), o);
 #pragma unroll
       for (int k = 0; k < N / 2; ++k) y[k] = fma2(o[k], ws[k], mul2(x[k], wc[k]));
-    } else {
+      if (w) {
+        u64 sq = mul2(x[0], x[0]);
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) y[k] = mul2(x[k], wc[k]);
-    }
-    if (w) {
+        for (int k = 1; k < N / 2; ++k) sq = fma2(x[k], x[k], sq);
+        float sum = lo_f(sq) + hi_f(sq);
 #pragma unroll
-      for (int k = 0; k < N / 2; ++k) y[k] = mul2(y[k], r2);
+        for (int d = LPR / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+        const u64 r2 = pack2(r, r);
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) y[k] = mul2(y[k], r2);
+      }
+      if (h + u * RPW < heads) Vec<T>::store(dst, u * RPW * p.D, y);
     }
-    if (h0 + u * RPW < heads) Vec<T>::store(dst, u * RPW * p.D, y);
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = next[u];
   }
 }
 
@@ -257,26 +280,36 @@ kvq_status launch(Params p, cudaStream_t s) {
                    (p.rot == 0 || (p.interleaved ? p.rot % N == 0
                                                  : p.rot % (2 * N) == 0 && aligned16(p.rope)));
   if (vec) {
-    // four loads a warp in flight where that leaves enough warps to fill the GPU
-    // (148 SMs of 32 warps), one where it would not: at 64 tokens of 40 heads
-    // the step is latency, and fewer heads a warp finish sooner
+    // A warp takes as many of a token's heads as still leaves 148 SMs 24 warps
+    // each: the angles and the weights are then formed for all of them.  Where
+    // even one chunk of four loads a warp leaves fewer, the step is latency and
+    // one load a warp finishes soonest.
     const int rpw = 32 / lpr;
-    auto units_of = [&](int rows) {
-      return static_cast<long long>(p.T) * ((p.H_q + rows - 1) / rows + (p.H_kv + rows - 1) / rows);
-    };
-    const bool many = units_of(4 * rpw) >= 148 * 32;
-    const long long grid = (units_of(many ? 4 * rpw : rpw) + warps - 1) / warps;
+    auto chunks_of = [&](int heads_of) { return (p.H_q + heads_of - 1) / heads_of + (p.H_kv + heads_of - 1) / heads_of; };
+    const bool many = static_cast<long long>(p.T) * chunks_of(4 * rpw) >= 148 * 24;
+    const int chunks = chunks_of(many ? 4 * rpw : rpw);
+    p.chunks = 1;
+    while (many && p.chunks < chunks &&
+           static_cast<long long>(p.T) * ((chunks + p.chunks) / (p.chunks + 1)) >= 148 * 24)
+      ++p.chunks;
+    const long long grid = (static_cast<long long>(p.T) * ((chunks + p.chunks - 1) / p.chunks) + warps - 1) / warps;
     if (grid > 0x3fffffffLL) return KVQ_ERR_UNSUPPORTED;
     cudaError_t e = cudaErrorInvalidValue;
     const dim3 g(static_cast<unsigned>(grid)), b(kThreads);
-    auto run = [&](auto one, auto four) { e = many ? launch_pdl(four, g, b, 0, s, p) : launch_pdl(one, g, b, 0, s, p); };
+    auto run = [&](auto lpr_c) {
+      constexpr int L = decltype(lpr_c)::value;
+      e = p.interleaved ? (many ? launch_pdl(qk_vec_kernel<T, L, 4, true>, g, b, 0, s, p)
+                                : launch_pdl(qk_vec_kernel<T, L, 1, true>, g, b, 0, s, p))
+                        : (many ? launch_pdl(qk_vec_kernel<T, L, 4, false>, g, b, 0, s, p)
+                                : launch_pdl(qk_vec_kernel<T, L, 1, false>, g, b, 0, s, p));
+    };
     switch (lpr) {
-      case 1: run(qk_vec_kernel<T, 1, 1>, qk_vec_kernel<T, 1, 4>); break;
-      case 2: run(qk_vec_kernel<T, 2, 1>, qk_vec_kernel<T, 2, 4>); break;
-      case 4: run(qk_vec_kernel<T, 4, 1>, qk_vec_kernel<T, 4, 4>); break;
-      case 8: run(qk_vec_kernel<T, 8, 1>, qk_vec_kernel<T, 8, 4>); break;
-      case 16: run(qk_vec_kernel<T, 16, 1>, qk_vec_kernel<T, 16, 4>); break;
-      case 32: run(qk_vec_kernel<T, 32, 1>, qk_vec_kernel<T, 32, 4>); break;
+      case 1: run(std::integral_constant<int, 1>{}); break;
+      case 2: run(std::integral_constant<int, 2>{}); break;
+      case 4: run(std::integral_constant<int, 4>{}); break;
+      case 8: run(std::integral_constant<int, 8>{}); break;
+      case 16: run(std::integral_constant<int, 16>{}); break;
+      case 32: run(std::integral_constant<int, 32>{}); break;
     }
     if (e != cudaSuccess) return KVQ_ERR_CUDA;
   } else {
