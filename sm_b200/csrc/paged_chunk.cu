@@ -355,12 +355,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       if (lane == 0) {
         const uint32_t idesc_qk = instr_desc(kBT, false);
         const uint32_t idesc_pv = instr_desc(D, true);
+        // descriptors: the address field counts 16-byte units, so a step adds to the low word
+        const uint64_t dq = smem_desc(base + M::kQ, 16, 1024), dk = smem_desc(base + M::kK, 16, 1024),
+                       dv = smem_desc(base + M::kV, kTileHalf, 1024);
         auto qk = [&](int t, uint32_t k) {
-          const uint32_t kt = base + M::kK + (k & 1u) * M::kTile;
+          const uint64_t q0 = dq + static_cast<uint64_t>(t * (M::kTile >> 4)), k0 = dk + static_cast<uint64_t>((k & 1u) * (M::kTile >> 4));
+#pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            const uint32_t q_addr = base + M::kQ + t * M::kTile + (i >> 2) * kTileHalf + (i & 3) * 32;
-            const uint32_t k_addr = kt + (i >> 2) * kTileHalf + (i & 3) * 32;
-            mma_ss(tmem + 128u * t, smem_desc(q_addr, 16, 1024), smem_desc(k_addr, 16, 1024), idesc_qk, i > 0);
+            const uint64_t step = static_cast<uint64_t>(((i >> 2) * kTileHalf + (i & 3) * 32) >> 4);
+            mma_ss(tmem + 128u * t, q0 + step, k0 + step, idesc_qk, i > 0);
           }
           mma_commit(bar(S_FULL + t));
         };
@@ -368,11 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         auto pv = [&](int t, bool first) {
           wait_bar(bar(P_FULL + t), done[t] & 1u, p.err, abort_flag);
           tc_fence_after();
-          for (int i = 0; i < kBT / 16; ++i) {
-            const uint32_t v_addr = base + M::kV + i * 16 * 128;
-            mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * i, smem_desc(v_addr, kTileHalf, 1024), idesc_pv,
+#pragma unroll
+          for (int i = 0; i < kBT / 16; ++i)
+            mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * i, dv + static_cast<uint64_t>(i * 128), idesc_pv,
                    (!first) || (i > 0));
-          }
           mma_commit(bar(PV_DONE + t));
           ++done[t];
         };
