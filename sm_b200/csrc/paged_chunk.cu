@@ -25,13 +25,16 @@
 // the same u / z in exact arithmetic.
 //
 // Warp roles (20 warps, 96 registers each):
-//   0        producer: lanes 0..3 copy 32 keys each (codes and scales) of a K
-//            or V unit into a ring; order K(0), K(1), V(0), K(2), V(1), ...
+//   0        producer: lanes 0 and 1 copy 32 keys each (codes and scales) of
+//            half a K or V block into a ring; order K(0), K(1), V(0), K(2), ...
 //   1        MMA issuer (one thread) and TMEM owner
 //   2        Q loader
 //   4..7     softmax of tile 0 (a thread a row), 8..11 of tile 1
-//   12..19   decode: warp w converts 16 keys of each unit
+//   12..19   decode: warp w converts 16 keys of each block, warps 12..15 from
+//            its first half-unit, 16..19 from its second
 //   3        idle
+// K and V tiles are both double: with one V tile the chain P V -> V free -> V
+// decoded -> P V paced every block.
 // TMEM columns: S/P of tile t at [128 t, +128), O at [256 + 128 t, +D).
 // Shared-memory tiles use the 128-byte-swizzled UMMA layout of tc_common.cuh.
 #include <cuda.h>
@@ -52,33 +55,33 @@ constexpr int kDecodeWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;
 constexpr int kTileHalf = kBT * 128;              // 16 KB: 128 rows x 64 bf16
-constexpr int kMaxUnits = 6;
+constexpr int kMaxUnits = 12;                    // half-units of the ring
 
 template <int D>
 struct Smem {
   static constexpr int kTile = D / 64 * kTileHalf;
   static constexpr int kQ = 0;                     // two row tiles
   static constexpr int kK = 2 * kTile;             // two K tiles
-  static constexpr int kV = kK + 2 * kTile;        // one V tile
-  static constexpr int kRing = kV + kTile;
-  static constexpr int kRingBytes = 54 * 1024;
+  static constexpr int kV = kK + 2 * kTile;        // two V tiles
+  static constexpr int kRing = kV + 2 * kTile;
+  static constexpr int kRingBytes = (D == 128 ? 27 : 54) * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 32 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kMisc = kBar + 40 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
   static constexpr int kPre = kMisc + 80;          // int pre[S + 1] (inline plan)
 };
 
 enum Bar {
   RING_FULL = 0,                 // [kMaxUnits]
-  RING_EMPTY = 6,                // [kMaxUnits]
-  K_READY = 12,                  // [2]
-  K_FREE = 14,                   // [2]
-  V_READY = 16,
-  V_FREE = 17,
-  Q_READY = 18,
-  Q_FREE = 19,
-  S_FULL = 20,                   // [2]
-  P_FULL = 22,                   // [2]
-  PV_DONE = 24,                  // [2]
+  RING_EMPTY = 12,               // [kMaxUnits]
+  K_READY = 24,                  // [2]
+  K_FREE = 26,                   // [2]
+  V_READY = 28,                  // [2]
+  V_FREE = 30,                   // [2]
+  S_FULL = 32,                   // [2]
+  P_FULL = 34,                   // [2]
+  PV_DONE = 36,                  // [2]
+  Q_READY = 38,
+  Q_FREE = 39,
 };
 
 struct Params {
@@ -159,11 +162,12 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
   constexpr int kCb = D * BITS / 8, QN = D / 16, TPP = 32 / QN;
   const int q = lane % QN, tt = lane / QN;
   const bool swap = D == 128 && (q & 4) != 0;
-  const float* sc = reinterpret_cast<const float*>(u + kBT * kCb);
+  const int w4 = wk & 3;                            // the warp's 16 keys within the half-unit
+  const float* sc = reinterpret_cast<const float*>(u + kBT / 2 * kCb);
   u64 ks[8];                                       // slot 4 i + r: pair r of 8-feature half i ^ swap
   if (!kV) {
     if (16 * wk < nv) {
-      const float4* s4 = reinterpret_cast<const float4*>(sc + (wk >> 1) * D + 16 * q);
+      const float4* s4 = reinterpret_cast<const float4*>(sc + (w4 >> 1) * D + 16 * q);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int ci = i ^ (swap ? 1 : 0);
@@ -181,12 +185,12 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
   const u64 mul = pack2(256.f, 16.f), add = pack2(-263.f, -23.f), sub = pack2(-8388735.f, -8388735.f);
 #pragma unroll 1
   for (int it = 0; it < 16 / TPP; ++it) {
-    const int t = 16 * wk + TPP * it + tt;
+    const int t = 16 * wk + TPP * it + tt, tu = 16 * w4 + TPP * it + tt;
     uint4 o[2];
     if (t < nv) {
       u64 s2 = 0ull;
       if (kV) {
-        float s = sc[D / 32 * t + (q >> 1)];
+        float s = sc[D / 32 * tu + (q >> 1)];
         if (!(fabsf(s) < INFINITY)) {              // remembered: rows that see the token become NaN
           atomicMax(s_bad, seg_key | static_cast<unsigned>(0x7fffffff - (t_base + t)));
           s = 0.f;
@@ -195,7 +199,7 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
       }
       uint32_t h[8];
       if (BITS == 4) {
-        const uint2 w2 = *reinterpret_cast<const uint2*>(u + t * kCb + 8 * q);
+        const uint2 w2 = *reinterpret_cast<const uint2*>(u + tu * kCb + 8 * q);
         const uint32_t w[2] = {swap ? w2.y : w2.x, swap ? w2.x : w2.y};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -206,7 +210,7 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
             h[4 * i + r] = pack_bf16(lo_f(x), hi_f(x));
           }
       } else {
-        const uint4 w4 = *reinterpret_cast<const uint4*>(u + t * kCb + 16 * q);
+        const uint4 w4 = *reinterpret_cast<const uint4*>(u + tu * kCb + 16 * q);
         const uint32_t w[4] = {swap ? w4.z : w4.x, swap ? w4.w : w4.y, swap ? w4.x : w4.z, swap ? w4.y : w4.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -269,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = p.t.H, G = p.t.G, TR = p.TT * G;
   constexpr int cb = D * BITS / 8;
-  constexpr int kScales = D * 16;                         // scale bytes of a unit (K: 4 groups x D; V: 128 x D / 32)
-  constexpr int unit_bytes = kBT * cb + kScales;
+  constexpr int kScales = D * 8;                          // scale bytes of a half-unit (K: 2 groups x D; V: 64 x D / 32)
+  constexpr int unit_bytes = kBT / 2 * cb + kScales;
   constexpr uint32_t nu = M::kRingBytes / unit_bytes < kMaxUnits ? M::kRingBytes / unit_bytes : kMaxUnits;
 
   if (!p.plan.count && warp == 0) warp_prefix(p.t, p.RI, kBT, s_pre);
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     for (int i = 0; i < 8; ++i) s_bad[i] = 0;
     for (uint32_t u = 0; u < nu; ++u) {
       mbar_init(bar(RING_FULL + u), 1);
-      mbar_init(bar(RING_EMPTY + u), kDecodeWarps);
+      mbar_init(bar(RING_EMPTY + u), kDecodeWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(K_READY + i), kDecodeWarps);
@@ -287,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init(bar(S_FULL + i), 1);
       mbar_init(bar(P_FULL + i), 4);
       mbar_init(bar(PV_DONE + i), 1);
+      mbar_init(bar(V_READY + i), kDecodeWarps);
+      mbar_init(bar(V_FREE + i), 1);
     }
-    mbar_init(bar(V_READY), kDecodeWarps);
-    mbar_init(bar(V_FREE), 1);
     mbar_init(bar(Q_READY), 1);
     mbar_init(bar(Q_FREE), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -309,126 +313,154 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   if (wr.g0 < wr.g1) {
     if (warp == 0) {
       // ======================= producer =======================
+      // A lane's page and row of a block, looked up a block ahead of its copies;
+      // V comes a block after K, from the same pages.
       Place kc = walk.begin(wr), vc = kc;
       uint32_t n = 0;
-      auto unit = [&](const Place& c, bool is_v) {
-        const uint32_t slot = n % nu;
-        const int t0 = c.j * kBT;
-        const int nv = min(kBT, c.s.len - t0);
-        const int pieces = (nv + 31) / 32;                // whole 32-key groups: a page holds them all
-        const uint32_t dst = base + M::kRing + slot * unit_bytes;
-        const uint32_t fb = bar(RING_FULL + slot);
-        int page = 0, at = 0;
-        if (lane < pieces) {
-          const int t = t0 + 32 * lane;
-          page = read_page(__ldg(p.t.table + static_cast<long long>(c.it.b) * p.t.max_pages + t / p.t.P), p.t.pages,
-                           p.err);
-          at = t % p.t.P;
-        }
-        if (lane == 0) {
-          if (n >= nu) wait_bar(bar(RING_EMPTY + slot), ((n / nu) - 1) & 1u, p.err, abort_flag);
-          mbar_expect_tx(fb, static_cast<uint32_t>(pieces * (32 * cb + kScales / 4)));
-        }
-        __syncwarp();
-        if (lane < pieces) {
-          const long long tok = (static_cast<long long>(page) * H + c.h) * p.t.P + at;
-          const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + tok * cb;
-          const float* scales = is_v ? p.v_scales + tok * (D / 32) : p.k_scales + tok / 32 * D;
-          bulk_g2s(dst + lane * 32 * cb, codes, 32 * cb, fb);
-          bulk_g2s(dst + kBT * cb + lane * (kScales / 4), scales, kScales / 4, fb);
-        }
-        __syncwarp();
-        ++n;
+      auto lookup = [&](const Place& c) {
+        const int t = c.j * kBT + 32 * lane;
+        return c.left > 0 && lane < 4 && t < c.s.len
+                   ? __ldg(p.t.table + static_cast<long long>(c.it.b) * p.t.max_pages + t / p.t.P)
+                   : 0;
       };
-      unit(kc, false);
-      walk.next(kc);
-      while (vc.left > 0) {
-        if (kc.left > 0) {
-          unit(kc, false);
-          walk.next(kc);
+      int next_page = lookup(kc), k_page = 0, v_page = 0;
+      auto unit = [&](const Place& c, bool is_v) {
+        const int t0 = c.j * kBT;
+        const int groups = (min(kBT, c.s.len - t0) + 31) / 32;   // whole 32-key groups: a page holds them all
+        const int page = is_v ? v_page : k_page, at = (t0 + 32 * lane) % p.t.P;
+        for (int half = 0; half < 2; ++half, ++n) {
+          const uint32_t slot = n % nu;
+          const int pieces = min(2, groups - 2 * half), i = lane - 2 * half;   // (a half past the end brings nothing)
+          const uint32_t dst = base + M::kRing + slot * unit_bytes;
+          const uint32_t fb = bar(RING_FULL + slot);
+          if (lane == 0) {
+            if (n >= nu) wait_bar(bar(RING_EMPTY + slot), ((n / nu) - 1) & 1u, p.err, abort_flag);
+            mbar_expect_tx(fb, static_cast<uint32_t>(max(pieces, 0) * (32 * cb + kScales / 2)));
+          }
+          __syncwarp();
+          if (i >= 0 && i < pieces) {
+            const long long tok = (static_cast<long long>(page) * H + c.h) * p.t.P + at;
+            const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + tok * cb;
+            const float* scales = is_v ? p.v_scales + tok * (D / 32) : p.k_scales + tok / 32 * D;
+            bulk_g2s(dst + i * 32 * cb, codes, 32 * cb, fb);
+            bulk_g2s(dst + kBT / 2 * cb + i * (kScales / 2), scales, kScales / 2, fb);
+          }
+          __syncwarp();
         }
+      };
+      auto k_unit = [&]() {
+        v_page = k_page;
+        k_page = read_page(next_page, p.t.pages, p.err);
+        Place ahead = kc;
+        walk.next(ahead);
+        next_page = lookup(ahead);
+        unit(kc, false);
+        kc = ahead;
+      };
+      k_unit();
+      while (vc.left > 0) {
+        const bool more = kc.left > 0;
+        if (more) k_unit();
+        else v_page = k_page;
         unit(vc, true);
         walk.next(vc);
       }
     } else if (warp == 1) {
       // ======================= MMA issuer =======================
-      if (lane == 0) {
-        const uint32_t idesc_qk = instr_desc(kBT, false);
-        const uint32_t idesc_pv = instr_desc(D, true);
-        // descriptors: the address field counts 16-byte units, so a step adds to the low word
-        const uint64_t dq = smem_desc(base + M::kQ, 16, 1024), dk = smem_desc(base + M::kK, 16, 1024),
-                       dv = smem_desc(base + M::kV, kTileHalf, 1024);
-        auto qk = [&](int t, uint32_t k) {
-          const uint64_t q0 = dq + static_cast<uint64_t>(t * (M::kTile >> 4)), k0 = dk + static_cast<uint64_t>((k & 1u) * (M::kTile >> 4));
+      // The whole warp runs this loop, on values that are the same in every
+      // lane (broadcast where they come from memory), and one lane issues: the
+      // operands of tcgen05.mma then sit in uniform registers.  With the loop
+      // in one lane's branch each instruction had to move its eight operands
+      // there first, and 32 of them a block took longer than their execution.
+      const uint32_t lead = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t idesc_qk = instr_desc(kBT, false);
+      const uint32_t idesc_pv = instr_desc(D, true);
+      // descriptors: the address field counts 16-byte units, so a step adds to the low word
+      const uint64_t dq = smem_desc(base + M::kQ, 16, 1024), dk = smem_desc(base + M::kK, 16, 1024),
+                     dv = smem_desc(base + M::kV, kTileHalf, 1024);
+      auto qk = [&](int t, uint32_t k) {
+        const uint64_t q0 = dq + static_cast<uint64_t>(t * (M::kTile >> 4)),
+                       k0 = dk + static_cast<uint64_t>((k & 1u) * (M::kTile >> 4));
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint64_t step = static_cast<uint64_t>(((i >> 2) * kTileHalf + (i & 3) * 32) >> 4);
-            mma_ss(tmem + 128u * t, q0 + step, k0 + step, idesc_qk, i > 0);
-          }
-          mma_commit(bar(S_FULL + t));
-        };
-        uint32_t done[2] = {0, 0};                          // P V products issued per tile
-        auto pv = [&](int t, bool first) {
-          wait_bar(bar(P_FULL + t), done[t] & 1u, p.err, abort_flag);
-          tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < kBT / 16; ++i)
-            mma_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * i, dv + static_cast<uint64_t>(i * 128), idesc_pv,
-                   (!first) || (i > 0));
-          mma_commit(bar(PV_DONE + t));
-          ++done[t];
-        };
-        // S of a tile overwrites its P: the last P V product must be done
-        auto pv_done = [&](int t) {
-          if (done[t] > 0) {
-            wait_bar(bar(PV_DONE + t), (done[t] - 1) & 1u, p.err, abort_flag);
-            tc_fence_after();
-          }
-        };
-        Place c = walk.begin(wr), cn = c;
-        uint32_t sq = 0;
-        wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
-        ++sq;
-        wait_bar(bar(K_READY), 0u, p.err, abort_flag);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t step = static_cast<uint64_t>(((i >> 2) * kTileHalf + (i & 3) * 32) >> 4);
+          mma_ss_if(lead, tm + 128u * t, q0 + step, k0 + step, idesc_qk, i > 0);
+        }
+        mma_commit_if(lead, bar(S_FULL + t));
+      };
+      uint32_t done[2] = {0, 0};                          // P V products issued per tile
+      auto pv = [&](int t, uint32_t k, bool first) {
+        const uint64_t v0 = dv + static_cast<uint64_t>((k & 1u) * (M::kTile >> 4));
+        wait_bar(bar(P_FULL + t), done[t] & 1u, p.err, abort_flag);
         tc_fence_after();
-        for (int t = 0; t < walk.tiles(c); ++t) qk(t, 0);
-        mma_commit(bar(K_FREE));
-        if (walk.last(c)) mma_commit(bar(Q_FREE));
-        walk.next(cn);
-        for (uint32_t k = 0; c.left > 0; ++k) {
-          const bool more = cn.left > 0, boundary = more && cn.start;
-          const bool two = walk.tiles(c) == 2;
-          wait_bar(bar(V_READY), k & 1u, p.err, abort_flag);
+#pragma unroll
+        for (int i = 0; i < kBT / 16; ++i)
+          mma_ts_if(lead, tm + 256u + 128u * t, tm + 128u * t + 8u * i, v0 + static_cast<uint64_t>(i * 128), idesc_pv,
+                    (!first) || (i > 0));
+        mma_commit_if(lead, bar(PV_DONE + t));
+        ++done[t];
+      };
+      // S of a tile overwrites its P: the last P V product must be done
+      auto pv_done = [&](int t) {
+        if (done[t] > 0) {
+          wait_bar(bar(PV_DONE + t), (done[t] - 1) & 1u, p.err, abort_flag);
           tc_fence_after();
-          pv(0, c.start);
-          if (more && !boundary) {
+        }
+      };
+      // what the loop asks about a block, in one word
+      enum : uint32_t { kMore = 1, kStart = 2, kTwo = 4, kLast = 8 };
+      Place c = walk.begin(wr);
+      auto flags = [&]() {
+        const uint32_t f = c.left > 0 ? kMore | (c.start ? kStart : 0u) | (walk.tiles(c) == 2 ? kTwo : 0u) |
+                                            (walk.last(c) ? kLast : 0u)
+                                      : 0u;
+        walk.next(c);
+        return __shfl_sync(0xffffffffu, f, 0);
+      };
+      uint32_t fc = flags(), fn = flags();                // the current block's and the next one's
+      uint32_t sq = 0;
+      wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
+      ++sq;
+      wait_bar(bar(K_READY), 0u, p.err, abort_flag);
+      tc_fence_after();
+      qk(0, 0);
+      if (fc & kTwo) qk(1, 0);
+      mma_commit_if(lead, bar(K_FREE));
+      if (fc & kLast) mma_commit_if(lead, bar(Q_FREE));
+      for (uint32_t k = 0; fc & kMore; ++k) {
+        const bool more = fn & kMore, boundary = more && (fn & kStart);
+        wait_bar(bar(V_READY + (k & 1u)), (k >> 1) & 1u, p.err, abort_flag);
+        tc_fence_after();
+        pv(0, k, fc & kStart);
+        const uint32_t fnn = flags();                     // while the product runs
+        if (more && !boundary) {
+          wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
+          pv_done(0);
+          tc_fence_after();
+          qk(0, k + 1);
+        }
+        if (fc & kTwo) pv(1, k, fc & kStart);
+        mma_commit_if(lead, bar(V_FREE + (k & 1u)));
+        if (more) {
+          if (boundary) {
+            wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
+            ++sq;
             wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
             pv_done(0);
             tc_fence_after();
             qk(0, k + 1);
           }
-          if (two) pv(1, c.start);
-          mma_commit(bar(V_FREE));
-          if (more) {
-            if (boundary) {
-              wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
-              ++sq;
-              wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
-              pv_done(0);
-              tc_fence_after();
-              qk(0, k + 1);
-            }
-            if (walk.tiles(cn) == 2) {
-              pv_done(1);
-              tc_fence_after();
-              qk(1, k + 1);
-            }
-            mma_commit(bar(K_FREE + ((k + 1) & 1u)));
-            if (walk.last(cn)) mma_commit(bar(Q_FREE));
+          if (fn & kTwo) {
+            pv_done(1);
+            tc_fence_after();
+            qk(1, k + 1);
           }
-          c = cn;
-          walk.next(cn);
+          mma_commit_if(lead, bar(K_FREE + ((k + 1) & 1u)));
+          if (fn & kLast) mma_commit_if(lead, bar(Q_FREE));
         }
+        fc = fn;
+        fn = fnn;
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -451,28 +483,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // ======================= decode =======================
       const int wk = warp - 12;
       Place kc = walk.begin(wr), vc = kc;
-      uint32_t n = 0, kb = 0, vb = 0, seg = 0;
+      const int half = wk >> 2;
+      uint32_t n = half, kb = 0, vb = 0, seg = 0;
       auto decode = [&](const Place& c, bool is_v) {
-        const uint32_t slot = n % nu;
+        const uint32_t slot = n % nu, x = is_v ? vb : kb;
         wait_bar(bar(RING_FULL + slot), (n / nu) & 1u, p.err, abort_flag);
-        if (!is_v && kb >= 2) wait_bar(bar(K_FREE + (kb & 1u)), ((kb >> 1) - 1) & 1u, p.err, abort_flag);
-        if (is_v && vb >= 1) wait_bar(bar(V_FREE), (vb - 1) & 1u, p.err, abort_flag);
+        if (x >= 2) wait_bar(bar((is_v ? V_FREE : K_FREE) + (x & 1u)), ((x >> 1) - 1) & 1u, p.err, abort_flag);
         const unsigned char* u = sm + M::kRing + slot * unit_bytes;
         const int t0 = c.j * kBT, nv = min(kBT, c.s.len - t0);
+        unsigned char* dst = sm + (is_v ? M::kV : M::kK) + (x & 1u) * M::kTile;
         if (is_v) {
           if (c.start) ++seg;
-          decode_unit<BITS, D, true>(u, sm + M::kV, wk, lane, nv, t0, static_cast<unsigned long long>(seg) << 32,
+          decode_unit<BITS, D, true>(u, dst, wk, lane, nv, t0, static_cast<unsigned long long>(seg) << 32,
                                      s_bad + (seg & 7u));
         } else {
-          decode_unit<BITS, D, false>(u, sm + M::kK + (kb & 1u) * M::kTile, wk, lane, nv, 0, 0, nullptr);
+          decode_unit<BITS, D, false>(u, dst, wk, lane, nv, 0, 0, nullptr);
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(is_v ? V_READY : K_READY + (kb & 1u)));
+          mbar_arrive(bar((is_v ? V_READY : K_READY) + (x & 1u)));
           mbar_arrive(bar(RING_EMPTY + slot));
         }
-        ++n;
+        n += 2;
         if (is_v) ++vb; else ++kb;
       };
       decode(kc, false);
