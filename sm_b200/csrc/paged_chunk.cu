@@ -19,14 +19,15 @@
 // through 0 * inf, so its token's scale is taken as zero in the tile and the
 // token is remembered: rows that do see it become NaN at the segment's end.
 //
-// The softmax's reference maximum is lazy: it moves, and O and z are rescaled,
+// The softmax reads S once.  Its reference maximum is lazy: it moves, and O and z are rescaled,
 // only when a block's maximum outruns it by more than 8 in log2 units.  Any
 // reference that never falls more than that below the running maximum gives
-// the same u / z in exact arithmetic.
+// the same u / z in exact arithmetic.  (Where it moves within a block, the p
+// already written are rescaled in place, which rounds them once more.)
 //
 // Warp roles (20 warps, 96 registers each):
-//   0        producer: lanes 0 and 1 copy 32 keys each (codes and scales) of
-//            half a K or V block into a ring; order K(0), K(1), V(0), K(2), ...
+//   0        producer: two lanes copy 32 keys each (codes and scales) of half a
+//            K or V block into a ring; order K(0), K(1), V(0), K(2), ...
 //   1        MMA issuer (one thread) and TMEM owner
 //   2        Q loader
 //   4..7     softmax of tile 0 (a thread a row), 8..11 of tile 1
@@ -66,22 +67,22 @@ struct Smem {
   static constexpr int kRing = kV + 2 * kTile;
   static constexpr int kRingBytes = (D == 128 ? 27 : 54) * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 40 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kMisc = kBar + 52 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
   static constexpr int kPre = kMisc + 80;          // int pre[S + 1] (inline plan)
 };
 
 enum Bar {
-  RING_FULL = 0,                 // [kMaxUnits]
-  RING_EMPTY = 12,               // [kMaxUnits]
-  K_READY = 24,                  // [2]
-  K_FREE = 26,                   // [2]
-  V_READY = 28,                  // [2]
-  V_FREE = 30,                   // [2]
-  S_FULL = 32,                   // [2]
-  P_FULL = 34,                   // [2]
-  PV_DONE = 36,                  // [2]
-  Q_READY = 38,
-  Q_FREE = 39,
+  RING_FULL = 0,                 // [kMaxUnits][2 halves]
+  RING_EMPTY = 24,               // [kMaxUnits]
+  K_READY = 36,                  // [2]
+  K_FREE = 38,                   // [2]
+  V_READY = 40,                  // [2]
+  V_FREE = 42,                   // [2]
+  S_FULL = 44,                   // [2]
+  P_FULL = 46,                   // [2]
+  PV_DONE = 48,                  // [2]
+  Q_READY = 50,
+  Q_FREE = 51,
 };
 
 struct Params {
@@ -235,25 +236,27 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
   }
 }
 
-// Maximum (kMin: minimum) of 64 raw scores held in registers.
+// Maximum (kMin: minimum) of 32 raw scores held in registers.
 template <bool kMin>
-__device__ __forceinline__ float row_extreme(const uint32_t (&sr)[64]) {
+__device__ __forceinline__ float row_extreme(const uint32_t (&sr)[32]) {
   auto f = [](uint32_t x) { return __uint_as_float(x); };
   auto op3 = [](float a, float b, float c) { return kMin ? min3(a, b, c) : max3(a, b, c); };
-  float acc[8];
+  float acc[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    acc[j] = op3(f(sr[j]), f(sr[8 + j]), f(sr[16 + j]));
-    acc[j] = op3(acc[j], f(sr[24 + j]), f(sr[32 + j]));
-    acc[j] = op3(acc[j], f(sr[40 + j]), f(sr[48 + j]));
+  for (int j = 0; j < 4; ++j) {
+    acc[j] = op3(f(sr[j]), f(sr[4 + j]), f(sr[8 + j]));
+    acc[j] = op3(acc[j], f(sr[12 + j]), f(sr[16 + j]));
+    acc[j] = op3(acc[j], f(sr[20 + j]), f(sr[24 + j]));
   }
-  const float a = op3(acc[0], acc[1], acc[2]);
-  const float b = op3(acc[3], acc[4], acc[5]);
-  const float c = op3(acc[6], acc[7], a);
-  float r = op3(b, c, f(sr[56]));
-#pragma unroll
-  for (int j = 57; j < 63; j += 2) r = op3(r, f(sr[j]), f(sr[j + 1]));
-  return op3(r, f(sr[63]), f(sr[63]));
+  const float a = op3(acc[0], acc[1], f(sr[28])), b = op3(acc[2], acc[3], f(sr[29]));
+  return op3(op3(a, b, f(sr[30])), f(sr[31]), f(sr[31]));
+}
+
+// After a time-out: waits (100 ms at most) for a copy that is still in flight.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try(bar, parity) && globaltimer() - t0 < 100000000ull) {
+  }
 }
 
 template <int BITS, int D>
@@ -282,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) s_bad[i] = 0;
     for (uint32_t u = 0; u < nu; ++u) {
-      mbar_init(bar(RING_FULL + u), 1);
+      mbar_init(bar(RING_FULL + 2 * u), 1);
+      mbar_init(bar(RING_FULL + 2 * u + 1), 1);
       mbar_init(bar(RING_EMPTY + u), kDecodeWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
@@ -328,16 +332,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         const int t0 = c.j * kBT;
         const int groups = (min(kBT, c.s.len - t0) + 31) / 32;   // whole 32-key groups: a page holds them all
         const int page = is_v ? v_page : k_page, at = (t0 + 32 * lane) % p.t.P;
-        for (int half = 0; half < 2; ++half, ++n) {
+        for (int half = 0; half < 2; ++half) {
           const uint32_t slot = n % nu;
           const int pieces = min(2, groups - 2 * half), i = lane - 2 * half;   // (a half past the end brings nothing)
           const uint32_t dst = base + M::kRing + slot * unit_bytes;
-          const uint32_t fb = bar(RING_FULL + slot);
+          const uint32_t fb = bar(RING_FULL + 2 * slot + half);
+          int stop = 0;
           if (lane == 0) {
             if (n >= nu) wait_bar(bar(RING_EMPTY + slot), ((n / nu) - 1) & 1u, p.err, abort_flag);
-            mbar_expect_tx(fb, static_cast<uint32_t>(max(pieces, 0) * (32 * cb + kScales / 2)));
+            stop = *abort_flag;                           // after a time-out nothing more is copied
+            if (!stop) mbar_expect_tx(fb, static_cast<uint32_t>(max(pieces, 0) * (32 * cb + kScales / 2)));
           }
-          __syncwarp();
+          if (__shfl_sync(0xffffffffu, stop, 0)) return;
+          ++n;
           if (i >= 0 && i < pieces) {
             const long long tok = (static_cast<long long>(page) * H + c.h) * p.t.P + at;
             const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + tok * cb;
@@ -365,6 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         unit(vc, true);
         walk.next(vc);
       }
+      // The decode warps took every copy before they ended, unless a wait ran
+      // out: then the last ones in flight are waited for here (again bounded),
+      // so that none writes into shared memory after the CTA has left it.
+      if (*abort_flag && lane == 0)
+        for (uint32_t i = n > nu ? n - nu : 0; i < n; ++i) {
+          const uint32_t b = bar(RING_FULL + 2 * (i % nu) + (i & 1u)), ph = (i / nu) >> (nu & 1u) & 1u;
+          drain(b, ph);
+        }
+      __syncwarp();
     } else if (warp == 1) {
       // ======================= MMA issuer =======================
       // The whole warp runs this loop, on values that are the same in every
@@ -470,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
           if (!c.start) continue;
           if (s > 0) wait_bar(bar(Q_FREE), (s - 1) & 1u, p.err, abort_flag);
+          if (*abort_flag) break;
           ++s;
           const int nt = walk.tiles(c), tok = c.s.q0 + c.it.r0 / G;
           mbar_expect_tx(bar(Q_READY), static_cast<uint32_t>(nt * (D / 64) * TR * 128));
@@ -478,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               tma_load_4d(base + M::kQ + t * M::kTile + half * kTileHalf, &qmap, 64 * half, 0, c.h, tok + t * p.TT,
                           bar(Q_READY));
         }
+        if (*abort_flag && s > 0) drain(bar(Q_READY), (s - 1) & 1u);
       }
     } else if (warp >= 12) {
       // ======================= decode =======================
@@ -487,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       uint32_t n = half, kb = 0, vb = 0, seg = 0;
       auto decode = [&](const Place& c, bool is_v) {
         const uint32_t slot = n % nu, x = is_v ? vb : kb;
-        wait_bar(bar(RING_FULL + slot), (n / nu) & 1u, p.err, abort_flag);
+        wait_bar(bar(RING_FULL + 2 * slot + half), (n / nu) >> (nu & 1u) & 1u, p.err, abort_flag);
         if (x >= 2) wait_bar(bar((is_v ? V_FREE : K_FREE) + (x & 1u)), ((x >> 1) - 1) & 1u, p.err, abort_flag);
         const unsigned char* u = sm + M::kRing + slot * unit_bytes;
         const int t0 = c.j * kBT, nv = min(kBT, c.s.len - t0);
@@ -546,52 +564,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (walk.tiles(c) <= tile) continue;
         wait_bar(bar(S_FULL + tile), k & 1u, p.err, abort_flag);
         tc_fence_after();
+        // One pass over S, 32 columns at a time: the columns' maximum, the
+        // reference if it has to move, p = exp2(s * qscale - m_ref) as bf16 over
+        // the columns already read.
         const int nv = min(kBT, lim - c.j * kBT);
-        // pass 1: the row's extreme over the columns it sees, 64 at a time
-        float mx = neg ? INFINITY : -INFINITY;
+        u64 z2 = 0ull;
 #pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t sr[64];
-          KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
-          KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+        for (int cc = 0; cc < 4; ++cc) {
+          const int left = nv - 32 * cc;                  // columns of these that the row sees
+          if (__all_sync(0xffffffffu, left <= 0)) {
+            uint32_t zero[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) zero[e] = 0u;
+            KVQ_ST16(s_col + 16u * cc, zero);
+            continue;
+          }
+          uint32_t sr[32];
+          KVQ_LD32(sr, s_col + 32u * cc);
           tmem_wait_ld();
-          if (nv < kBT) {
+          const bool whole = __all_sync(0xffffffffu, left >= 32);
+          if (!whole) {
             const uint32_t fill = __float_as_uint(neg ? INFINITY : -INFINITY);
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (64 * hh + e >= nv) sr[e] = fill;
+            for (int e = 0; e < 32; ++e)
+              if (e >= left) sr[e] = fill;
           }
-          mx = neg ? fminf(mx, row_extreme<true>(sr)) : fmaxf(mx, row_extreme<false>(sr));
-        }
-        // (a row that sees no column keeps mx = -inf, or +inf under a negative scale: never a new reference)
-        const float mb = nv > 0 ? mx * p.qscale : -INFINITY;
-        const bool need = mb > m_ref + kLazy;
-        const float m_new = need ? mb : m_ref;
-        const float a = need ? ex2(m_ref - m_new) : 1.f;  // 0 on the first block
-        z *= a;
-        m_ref = m_new;
-        if (__any_sync(0xffffffffu, need) && !c.start) {
+          const float mx = neg ? row_extreme<true>(sr) : row_extreme<false>(sr);
+          const float mb = left > 0 ? mx * p.qscale : -INFINITY;
+          const bool need = mb > m_ref + kLazy;
+          if (__any_sync(0xffffffffu, need)) {
+            const float a = need ? ex2(m_ref - mb) : 1.f;  // 0 where the row had no key
+            if (need) m_ref = mb;
+            z *= a;
+            z2 = mul2(z2, pack2(a, a));
+            if (!c.start) {
 #pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t orr[32];
-            KVQ_LD32(orr, o_col + 32u * cc);
-            tmem_wait_ld();
+              for (int oc = 0; oc < D / 16; ++oc) {
+                uint32_t orr[16];
+                KVQ_LD16(orr, o_col + 16u * oc);
+                tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
-            KVQ_ST32(o_col + 32u * cc, orr);
-          }
-        }
-        // pass 2: p = exp2(s * qscale - m_ref) as bf16 over the S columns; a
-        // block that every row of the warp sees whole needs no masking
-        const u64 qs2 = pack2(p.qscale, p.qscale), nm2 = pack2(-m_ref, -m_ref);
-        u64 z2 = 0ull;
-        if (__all_sync(0xffffffffu, nv >= kBT)) {
+                for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+                KVQ_ST16(o_col + 16u * oc, orr);
+              }
+            }
 #pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t sr[32];
-            KVQ_LD32(sr, s_col + 32u * cc);
-            tmem_wait_ld();
-            uint32_t pk[16];
+            for (int pc = 0; pc < cc; ++pc) {              // the block's p so far
+              uint32_t pk[16];
+              KVQ_LD16(pk, s_col + 16u * pc);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                pk[e] = pack_bf16(__uint_as_float(pk[e] << 16) * a, __uint_as_float(pk[e] & 0xFFFF0000u) * a);
+              KVQ_ST16(s_col + 16u * pc, pk);
+            }
+          }
+          const u64 qs2 = pack2(p.qscale, p.qscale), nm2 = pack2(-m_ref, -m_ref);
+          uint32_t pk[16];
+          if (whole) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
@@ -599,25 +629,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
               z2 = add2(z2, pack2(p0, p1));
               pk[e] = pack_bf16(p0, p1);
             }
-            KVQ_ST16(s_col + 16u * cc, pk);
-          }
-        } else {
-#pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t sr[32];
-            KVQ_LD32(sr, s_col + 32u * cc);
-            tmem_wait_ld();
-            uint32_t pk[16];
+          } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
-              const float p0 = 32 * cc + 2 * e < nv ? ex2(lo_f(x)) : 0.f;
-              const float p1 = 32 * cc + 2 * e + 1 < nv ? ex2(hi_f(x)) : 0.f;
+              const float p0 = 2 * e < left ? ex2(lo_f(x)) : 0.f;
+              const float p1 = 2 * e + 1 < left ? ex2(hi_f(x)) : 0.f;
               z2 = add2(z2, pack2(p0, p1));
               pk[e] = pack_bf16(p0, p1);
             }
-            KVQ_ST16(s_col + 16u * cc, pk);
           }
+          KVQ_ST16(s_col + 16u * cc, pk);
         }
         z += lo_f(z2) + hi_f(z2);
         tmem_wait_st();

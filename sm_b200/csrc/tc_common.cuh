@@ -136,6 +136,15 @@ __device__ __forceinline__ void mma_commit_if(uint32_t on, uint32_t bar) {
         "=r"(r[29]), "=r"(r[30]), "=r"(r[31])                                                           \
       : "r"(taddr))
 
+#define KVQ_LD16(r, taddr)                                                                             \
+  asm volatile(                                                                                        \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}," \
+      " [%16];"                                                                                        \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), \
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),        \
+        "=r"(r[15])                                                                                     \
+      : "r"(taddr))
+
 // the same, into r[o .. o + 31] of a larger register array
 #define KVQ_LD32_AT(r, o, taddr)                                                                       \
   asm volatile(                                                                                        \

@@ -1,0 +1,244 @@
+"""The paged chunk kernel's synchronization protocol, as a model on the CPU
+(the machine of test_chunk_protocol: hardware parity semantics for every wait,
+copies and MMAs that complete out of order, a version on every buffer).
+
+What differs from the contiguous kernel: the ring holds half-units of 64 keys,
+each decoded by four of the eight decode warps; V tiles are double; and a
+segment's item has one or two row tiles, so the second tile's barriers count
+its own blocks.  A ring of odd length gives a slot to the two halves in turn,
+and a decode warp sees only its own half's uses of it: the slot's full barrier
+is one per half, since on a shared one a warp would wait for a phase without
+having seen the one before, and a parity wait cannot tell those apart."""
+
+import pytest
+
+from tests.test_chunk_protocol import Bar, Model
+
+DW, RW = 8, 4
+
+
+class PagedModel(Model):
+    """blocks: [(segment, first, last, tiles)]."""
+
+    def __init__(self, blocks, n_units, seed, lag):
+        super().__init__(blocks, 2, n_units, seed, lag)
+        for u in range(n_units):
+            self.B[("RE", u)] = Bar(DW // 2)
+            for half in range(2):
+                self.B[("RF", u, half)] = Bar(1)
+        for i in range(2):
+            self.B[("VR", i)] = Bar(DW)
+            self.B[("VF", i)] = Bar(1)
+
+
+def roles_of(m, drop=None, shift=None, shared_full=False):
+    blocks, nu = m.blocks, m.nu
+
+    def full(n):
+        """Barrier and phase of half-unit n's arrival."""
+        if shared_full:
+            return ("RF", n % nu), n // nu
+        return ("RF", n % nu, n % 2), (n // nu) // (2 if nu % 2 else 1)
+
+    nb = len(blocks)
+    segs = []
+    for b in blocks:
+        if b[1]:
+            segs.append([])
+        segs[-1].append(b)
+    seg_blocks = [[i for i, b in enumerate(blocks) if b[0] == s[0][0]] for s in segs]
+    tiles = [b[3] for b in blocks]
+    # a tile's own count of the blocks before k
+    nth = [[sum(1 for x in tiles[:k] if x > t) for k in range(nb)] for t in range(2)]
+    units = [("K", 0)]
+    for v in range(nb):
+        if v + 1 < nb:
+            units.append(("K", v + 1))
+        units.append(("V", v))
+
+    def wait(name, bar, k):
+        return [] if drop == name else [("wait", bar, k + (shift == name))]
+
+    def producer():
+        n = 0
+        for typ, blk in units:
+            for half in range(2):
+                slot = n % nu
+                if n >= nu:
+                    yield from wait("ring_empty", ("RE", slot), n // nu - 1)
+                yield ("expect_tx", full(n)[0])
+                yield ("copy", full(n)[0], lambda slot=slot, v=(typ, blk, half): m.write(
+                    ("ring", slot), v, lambda p: {("dec", w) for w in range(4 * p[2], 4 * p[2] + 4)}))
+                n += 1
+
+    def qloader():
+        for s in range(len(segs)):
+            if s > 0:
+                yield from wait("q_free", "QF", s - 1)
+            yield ("expect_tx", "QR")
+            yield ("copy", "QR", lambda s=s: m.write(
+                "Q", s, lambda p: {("qk", t, i) for i in seg_blocks[p] for t in range(tiles[i])}))
+
+    def decode(w):
+        half = w // 4
+        n = half
+        count = {"K": 0, "V": 0}
+        for typ, blk in units:
+            slot, x = n % nu, count[typ]
+            yield from wait("ring_full", *full(n))
+            if x >= 2:
+                name = "k_free" if typ == "K" else "v_free"
+                yield from wait(name, (("KF" if typ == "K" else "VF"), x & 1), (x >> 1) - 1)
+            readers = ((lambda p: {("qk", t, p) for t in range(tiles[p])}) if typ == "K"
+                       else (lambda p: {("pv", t, p) for t in range(tiles[p])}))
+            yield ("do", lambda slot=slot, v=(typ, blk, half), readers=readers: (
+                m.read(("ring", slot), v, ("dec", w)),
+                m.write((v[0], v[1] & 1, w), v[1], readers)))
+            yield ("arrive", (("KR" if typ == "K" else "VR"), x & 1))
+            yield ("arrive", ("RE", slot))
+            n += 2
+            count[typ] += 1
+
+    def qk(t, k):
+        def fn():
+            m.read("Q", next(i for i, s in enumerate(seg_blocks) if k in s), ("qk", t, k))
+            for w in range(DW):
+                m.read(("K", k & 1, w), k, ("qk", t, k))
+            m.write(("S", t), k, lambda p: {("pv", t, p)} | {("sm", t, p, w) for w in range(RW)})
+        return [("mma", ("S", t), fn), ("commit", ("SF", t))]
+
+    def pv(t, k):
+        def fn():
+            for w in range(RW):
+                m.read(("P", t, w), k, ("pv", t, k))
+            for w in range(DW):
+                m.read(("V", k & 1, w), k, ("pv", t, k))
+            m.reads.setdefault(("S", t), set()).add(("pv", t, k))
+            for w in range(RW):
+                o = ("O", t, w)
+                if blocks[k][1]:
+                    prev = m.buf.get(o)
+                    assert prev is None or ("epi", t, prev) in m.reads.get(o, set()), "O overwritten unread"
+                else:
+                    assert m.buf.get(o) == k - 1, f"P V({k}) accumulates onto O v{m.buf.get(o)}"
+                m.buf[o] = k
+                m.reads[o] = set()
+        return [("mma", ("O", t), fn), ("commit", ("PD", t))]
+
+    def mma():
+        done = [0, 0]
+
+        def product(t, k):
+            yield from wait("p_full", ("PF", t), done[t])
+            yield from pv(t, k)
+            done[t] += 1
+
+        def pv_done(t):
+            if done[t] > 0:
+                yield from wait("pv_done", ("PD", t), done[t] - 1)
+
+        yield from wait("q_ready", "QR", 0)
+        sq = 1
+        yield from wait("k_ready", ("KR", 0), 0)
+        for t in range(tiles[0]):
+            yield from qk(t, 0)
+        yield ("commit", ("KF", 0))
+        if blocks[0][2]:
+            yield ("commit", "QF")
+        for k in range(nb):
+            nxt = k + 1 < nb
+            boundary = nxt and blocks[k + 1][1]
+            yield from wait("v_ready", ("VR", k & 1), k >> 1)
+            yield from product(0, k)
+            if nxt and not boundary:
+                yield from wait("k_ready", ("KR", (k + 1) & 1), (k + 1) >> 1)
+                yield from pv_done(0)
+                yield from qk(0, k + 1)
+            if tiles[k] == 2:
+                yield from product(1, k)
+            yield ("commit", ("VF", k & 1))
+            if nxt:
+                if boundary:
+                    yield from wait("q_ready", "QR", sq)
+                    sq += 1
+                    yield from wait("k_ready", ("KR", (k + 1) & 1), (k + 1) >> 1)
+                    yield from pv_done(0)
+                    yield from qk(0, k + 1)
+                if tiles[k + 1] == 2:
+                    yield from pv_done(1)
+                    yield from qk(1, k + 1)
+                yield ("commit", ("KF", (k + 1) & 1))
+                if blocks[k + 1][2]:
+                    yield ("commit", "QF")
+
+    def softmax(t, w):
+        for k in range(nb):
+            if tiles[k] <= t:
+                continue
+            n = nth[t][k]
+            yield from wait("s_full", ("SF", t), n)
+
+            def f(k=k):
+                m.read(("S", t), k, ("sm", t, k, w))
+                if not blocks[k][1]:
+                    assert m.buf.get(("O", t, w)) == k - 1, "rescale before the previous P V finished"
+                m.buf[("P", t, w)] = k
+            yield ("do", f)
+            yield ("arrive", ("PF", t))
+            if blocks[k][2]:
+                yield from wait("epilogue_pv", ("PD", t), n)
+                yield ("do", lambda k=k: m.read(("O", t, w), k, ("epi", t, k)))
+
+    roles = {"producer": producer(), "q": qloader(), "mma": mma()}
+    for w in range(DW):
+        roles[f"decode{w}"] = decode(w)
+    for t in range(2):
+        for w in range(RW):
+            roles[f"softmax{t}.{w}"] = softmax(t, w)
+    return roles
+
+
+def block_list(segments):
+    """segments: [(blocks, tiles)]."""
+    return [(s, j == 0, j == n - 1, t) for s, (n, t) in enumerate(segments) for j in range(n)]
+
+
+SEGMENTS = [[(1, 1)], [(1, 2)], [(3, 2)], [(28, 2)], [(5, 2), (23, 2)], [(1, 1), (1, 2), (1, 1), (1, 2)],
+            [(27, 2), (1, 1)], [(1, 2), (27, 1)], [(2, 2), (2, 1), (2, 2), (2, 1), (3, 2)], [(13, 1), (14, 1)]]
+
+
+@pytest.mark.parametrize("segments", SEGMENTS, ids=lambda s: "-".join(f"{n}x{t}" for n, t in s))
+@pytest.mark.parametrize("n_units", [3, 5, 11, 12])
+def test_protocol_holds(segments, n_units):
+    for seed in range(10):
+        m = PagedModel(block_list(segments), n_units, seed, lag=(seed % 4) * 0.3)
+        m.run(roles_of(m))
+
+
+@pytest.mark.parametrize("drop", ["ring_empty", "q_free", "k_free", "v_free", "pv_done", "epilogue_pv",
+                                  "p_full", "v_ready", "k_ready", "s_full"])
+def test_every_wait_is_needed(drop):
+    for segments in ([(3, 2)], [(5, 2), (23, 2)], [(27, 2), (1, 1)], [(9, 1), (9, 2), (9, 1)]):
+        for seed in range(60):
+            m = PagedModel(block_list(segments), 3, seed, lag=(seed % 4) * 0.3)
+            try:
+                m.run(roles_of(m, drop=drop))
+            except AssertionError:
+                return
+    raise AssertionError(f"leaving out the {drop} wait went unnoticed")
+
+
+@pytest.mark.parametrize("shift", ["ring_empty", "ring_full", "k_free", "v_free", "pv_done", "p_full",
+                                   "v_ready", "k_ready", "s_full", "q_ready"])
+def test_every_phase_is_right(shift):
+    with pytest.raises(AssertionError):
+        for seed in range(10):
+            m = PagedModel(block_list([(5, 2), (23, 2)]), 3, seed, lag=0.3)
+            m.run(roles_of(m, shift=shift))
+
+
+def test_a_full_barrier_shared_by_the_halves_of_an_odd_ring_aliases():
+    with pytest.raises(AssertionError, match="parity alias"):
+        for seed in range(200):
+            m = PagedModel(block_list([(28, 2)]), 3, seed, lag=(seed % 4) * 0.3)
+            m.run(roles_of(m, shared_full=True))
