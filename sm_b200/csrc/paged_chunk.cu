@@ -34,8 +34,10 @@
 //   12..19   decode: warp w converts 16 keys of each block, warps 12..15 from
 //            its first half-unit, 16..19 from its second
 //   3        idle
-// K and V tiles are both double: with one V tile the chain P V -> V free -> V
-// decoded -> P V paced every block.
+// K tiles are double, V has one: a second V tile leaves 27 KB for the ring, and
+// the copies' latency then costs more than the wait for V's turn (a ring of 59
+// KB and one V tile: 104 us for 4 x 64 rows over 16384 keys; 27 KB and two: 107;
+// at 8 bits, prompts: 348 against 369 us).
 // TMEM columns: S/P of tile t at [128 t, +128), O at [256 + 128 t, +D).
 // Shared-memory tiles use the 128-byte-swizzled UMMA layout of tc_common.cuh.
 #include <cuda.h>
@@ -63,11 +65,11 @@ struct Smem {
   static constexpr int kTile = D / 64 * kTileHalf;
   static constexpr int kQ = 0;                     // two row tiles
   static constexpr int kK = 2 * kTile;             // two K tiles
-  static constexpr int kV = kK + 2 * kTile;        // two V tiles
-  static constexpr int kRing = kV + 2 * kTile;
-  static constexpr int kRingBytes = (D == 128 ? 27 : 54) * 1024;
+  static constexpr int kV = kK + 2 * kTile;        // one V tile
+  static constexpr int kRing = kV + kTile;
+  static constexpr int kRingBytes = 59 * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 52 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kMisc = kBar + 50 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
   static constexpr int kPre = kMisc + 80;          // int pre[S + 1] (inline plan)
 };
 
@@ -76,13 +78,13 @@ enum Bar {
   RING_EMPTY = 24,               // [kMaxUnits]
   K_READY = 36,                  // [2]
   K_FREE = 38,                   // [2]
-  V_READY = 40,                  // [2]
-  V_FREE = 42,                   // [2]
-  S_FULL = 44,                   // [2]
-  P_FULL = 46,                   // [2]
-  PV_DONE = 48,                  // [2]
-  Q_READY = 50,
-  Q_FREE = 51,
+  V_READY = 40,
+  V_FREE = 41,
+  S_FULL = 42,                   // [2]
+  P_FULL = 44,                   // [2]
+  PV_DONE = 46,                  // [2]
+  Q_READY = 48,
+  Q_FREE = 49,
 };
 
 struct Params {
@@ -295,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init(bar(S_FULL + i), 1);
       mbar_init(bar(P_FULL + i), 4);
       mbar_init(bar(PV_DONE + i), 1);
-      mbar_init(bar(V_READY + i), kDecodeWarps);
-      mbar_init(bar(V_FREE + i), 1);
     }
+    mbar_init(bar(V_READY), kDecodeWarps);
+    mbar_init(bar(V_FREE), 1);
     mbar_init(bar(Q_READY), 1);
     mbar_init(bar(Q_FREE), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -317,60 +319,81 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   if (wr.g0 < wr.g1) {
     if (warp == 0) {
       // ======================= producer =======================
-      // A lane's page and row of a block, looked up a block ahead of its copies;
-      // V comes a block after K, from the same pages.
-      Place kc = walk.begin(wr), vc = kc;
-      uint32_t n = 0;
-      auto lookup = [&](const Place& c) {
-        const int t = c.j * kBT + 32 * lane;
-        return c.left > 0 && lane < 4 && t < c.s.len
-                   ? __ldg(p.t.table + static_cast<long long>(c.it.b) * p.t.max_pages + t / p.t.P)
-                   : 0;
+      // Lane i < 4 brings keys 32 i .. 32 i + 31 of a block (32 keys lie in one
+      // page); lanes 0, 1 fill the first half-unit, 2, 3 the second.  What the
+      // loop needs of a block is carried along from the one before: this one warp
+      // has to be through with four half-units in less time than a block takes
+      // (with divisions and 64-bit products per half it took 3.2k cycles itself).
+      const int half = (lane >> 1) & 1, P = p.t.P;
+      const int step_pages = kBT / P, step_rows = kBT % P;
+      const long long head_tokens = P, page_tokens = static_cast<long long>(H) * P;
+      Place kc = walk.begin(wr);
+      int pi = 0, at = 0, page = 0, left = 0;             // this lane's page index, row, page; keys from its first on
+      const int32_t* table = p.t.table;
+      auto look = [&]() {                                 // page of block kc for this lane
+        if (kc.left <= 0) return;
+        if (kc.start) {
+          const int t = kc.j * kBT + 32 * lane;
+          pi = t / P;
+          at = t - pi * P;
+          left = kc.s.len - t;
+          table = p.t.table + static_cast<long long>(kc.it.b) * p.t.max_pages;
+        } else {
+          pi += step_pages;
+          at += step_rows;
+          if (at >= P) {
+            at -= P;
+            ++pi;
+          }
+          left -= kBT;
+        }
+        page = lane < 4 && left > 0 ? __ldg(table + pi) : 0;
       };
-      int next_page = lookup(kc), k_page = 0, v_page = 0;
-      auto unit = [&](const Place& c, bool is_v) {
-        const int t0 = c.j * kBT;
-        const int groups = (min(kBT, c.s.len - t0) + 31) / 32;   // whole 32-key groups: a page holds them all
-        const int page = is_v ? v_page : k_page, at = (t0 + 32 * lane) % p.t.P;
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t slot = n % nu;
-          const int pieces = min(2, groups - 2 * half), i = lane - 2 * half;   // (a half past the end brings nothing)
-          const uint32_t dst = base + M::kRing + slot * unit_bytes;
-          const uint32_t fb = bar(RING_FULL + 2 * slot + half);
-          int stop = 0;
-          if (lane == 0) {
-            if (n >= nu) wait_bar(bar(RING_EMPTY + slot), ((n / nu) - 1) & 1u, p.err, abort_flag);
-            stop = *abort_flag;                           // after a time-out nothing more is copied
-            if (!stop) mbar_expect_tx(fb, static_cast<uint32_t>(max(pieces, 0) * (32 * cb + kScales / 2)));
-          }
-          if (__shfl_sync(0xffffffffu, stop, 0)) return;
-          ++n;
-          if (i >= 0 && i < pieces) {
-            const long long tok = (static_cast<long long>(page) * H + c.h) * p.t.P + at;
-            const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + tok * cb;
-            const float* scales = is_v ? p.v_scales + tok * (D / 32) : p.k_scales + tok / 32 * D;
-            bulk_g2s(dst + i * 32 * cb, codes, 32 * cb, fb);
-            bulk_g2s(dst + kBT / 2 * cb + i * (kScales / 2), scales, kScales / 2, fb);
-          }
-          __syncwarp();
+      look();
+      uint32_t n = 0, slot = half, wraps = 0;             // half-units issued; this half's slot and its rounds
+      auto unit = [&](bool is_v, long long tok, int groups) {
+        if (lane < 4 && wraps > 0) wait_bar(bar(RING_EMPTY + slot), (wraps - 1) & 1u, p.err, abort_flag);
+        if (__any_sync(0xffffffffu, *abort_flag)) return;   // after a time-out nothing more is copied
+        const uint32_t fb = bar(RING_FULL + 2 * slot + half);
+        if ((lane & ~2) == 0)                             // (a half past the end brings nothing)
+          mbar_expect_tx(fb, static_cast<uint32_t>(min(max(groups - lane, 0), 2) * (32 * cb + kScales / 2)));
+        __syncwarp();
+        if (lane < groups) {
+          const uint32_t dst = base + M::kRing + slot * unit_bytes, i = lane & 1;
+          const uint8_t* codes = (is_v ? p.v_codes : p.k_codes) + tok * cb;
+          const float* scales = is_v ? p.v_scales + tok * (D / 32) : p.k_scales + (tok >> 5) * D;
+          bulk_g2s(dst + i * 32 * cb, codes, 32 * cb, fb);
+          bulk_g2s(dst + kBT / 2 * cb + i * (kScales / 2), scales, kScales / 2, fb);
+        }
+        n += 2;
+        slot += 2;
+        if (slot >= nu) {
+          slot -= nu;
+          ++wraps;
         }
       };
+      long long tok_v = 0, tok = 0;
+      int groups_v = 0, groups = 0;
+      int blocks = static_cast<int>(wr.g1 - wr.g0), k_left = blocks;
       auto k_unit = [&]() {
-        v_page = k_page;
-        k_page = read_page(next_page, p.t.pages, p.err);
-        Place ahead = kc;
-        walk.next(ahead);
-        next_page = lookup(ahead);
-        unit(kc, false);
-        kc = ahead;
+        tok_v = tok;
+        groups_v = groups;
+        tok = read_page(page, p.t.pages, p.err) * page_tokens + kc.h * head_tokens + at;
+        groups = (min(kBT, __shfl_sync(0xffffffffu, left, 0)) + 31) >> 5;
+        walk.next(kc);
+        look();
+        unit(false, tok, groups);
+        --k_left;
       };
       k_unit();
-      while (vc.left > 0) {
-        const bool more = kc.left > 0;
-        if (more) k_unit();
-        else v_page = k_page;
-        unit(vc, true);
-        walk.next(vc);
+      for (; blocks > 0; --blocks) {
+        if (k_left > 0) {
+          k_unit();
+        } else {
+          tok_v = tok;
+          groups_v = groups;
+        }
+        unit(true, tok_v, groups_v);
       }
       // The decode warps took every copy before they ended, unless a wait ran
       // out: then the last ones in flight are waited for here (again bounded),
@@ -406,13 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         mma_commit_if(lead, bar(S_FULL + t));
       };
       uint32_t done[2] = {0, 0};                          // P V products issued per tile
-      auto pv = [&](int t, uint32_t k, bool first) {
-        const uint64_t v0 = dv + static_cast<uint64_t>((k & 1u) * (M::kTile >> 4));
+      auto pv = [&](int t, bool first) {
         wait_bar(bar(P_FULL + t), done[t] & 1u, p.err, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < kBT / 16; ++i)
-          mma_ts_if(lead, tm + 256u + 128u * t, tm + 128u * t + 8u * i, v0 + static_cast<uint64_t>(i * 128), idesc_pv,
+          mma_ts_if(lead, tm + 256u + 128u * t, tm + 128u * t + 8u * i, dv + static_cast<uint64_t>(i * 128), idesc_pv,
                     (!first) || (i > 0));
         mma_commit_if(lead, bar(PV_DONE + t));
         ++done[t];
@@ -446,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       if (fc & kLast) mma_commit_if(lead, bar(Q_FREE));
       for (uint32_t k = 0; fc & kMore; ++k) {
         const bool more = fn & kMore, boundary = more && (fn & kStart);
-        wait_bar(bar(V_READY + (k & 1u)), (k >> 1) & 1u, p.err, abort_flag);
+        wait_bar(bar(V_READY), k & 1u, p.err, abort_flag);
         tc_fence_after();
-        pv(0, k, fc & kStart);
+        pv(0, fc & kStart);
         const uint32_t fnn = flags();                     // while the product runs
         if (more && !boundary) {
           wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
@@ -456,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           tc_fence_after();
           qk(0, k + 1);
         }
-        if (fc & kTwo) pv(1, k, fc & kStart);
-        mma_commit_if(lead, bar(V_FREE + (k & 1u)));
+        if (fc & kTwo) pv(1, fc & kStart);
+        mma_commit_if(lead, bar(V_FREE));
         if (more) {
           if (boundary) {
             wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
@@ -502,14 +524,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       const int wk = warp - 12;
       Place kc = walk.begin(wr), vc = kc;
       const int half = wk >> 2;
-      uint32_t n = half, kb = 0, vb = 0, seg = 0;
+      uint32_t slot = half, wraps = 0, kb = 0, vb = 0, seg = 0;
       auto decode = [&](const Place& c, bool is_v) {
-        const uint32_t slot = n % nu, x = is_v ? vb : kb;
-        wait_bar(bar(RING_FULL + 2 * slot + half), (n / nu) >> (nu & 1u) & 1u, p.err, abort_flag);
-        if (x >= 2) wait_bar(bar((is_v ? V_FREE : K_FREE) + (x & 1u)), ((x >> 1) - 1) & 1u, p.err, abort_flag);
+        const uint32_t x = is_v ? vb : kb;
+        wait_bar(bar(RING_FULL + 2 * slot + half), wraps >> (nu & 1u) & 1u, p.err, abort_flag);
+        const uint32_t buf = is_v ? 0 : x & 1u;
+        if (is_v && x >= 1) wait_bar(bar(V_FREE), (x - 1) & 1u, p.err, abort_flag);
+        if (!is_v && x >= 2) wait_bar(bar(K_FREE + buf), ((x >> 1) - 1) & 1u, p.err, abort_flag);
         const unsigned char* u = sm + M::kRing + slot * unit_bytes;
         const int t0 = c.j * kBT, nv = min(kBT, c.s.len - t0);
-        unsigned char* dst = sm + (is_v ? M::kV : M::kK) + (x & 1u) * M::kTile;
+        unsigned char* dst = sm + (is_v ? M::kV : M::kK) + buf * M::kTile;
         if (is_v) {
           if (c.start) ++seg;
           decode_unit<BITS, D, true>(u, dst, wk, lane, nv, t0, static_cast<unsigned long long>(seg) << 32,
@@ -520,10 +544,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar((is_v ? V_READY : K_READY) + (x & 1u)));
+          mbar_arrive(bar((is_v ? V_READY : K_READY) + buf));
           mbar_arrive(bar(RING_EMPTY + slot));
         }
-        n += 2;
+        slot += 2;
+        if (slot >= nu) {
+          slot -= nu;
+          ++wraps;
+        }
         if (is_v) ++vb; else ++kb;
       };
       decode(kc, false);

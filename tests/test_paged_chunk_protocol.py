@@ -3,8 +3,7 @@
 copies and MMAs that complete out of order, a version on every buffer).
 
 What differs from the contiguous kernel: the ring holds half-units of 64 keys,
-each decoded by four of the eight decode warps; V tiles are double; and a
-segment's item has one or two row tiles, so the second tile's barriers count
+each decoded by four of the eight decode warps; and a segment's item has one or two row tiles, so the second tile's barriers count
 its own blocks.  A ring of odd length gives a slot to the two halves in turn,
 and a decode warp sees only its own half's uses of it: the slot's full barrier
 is one per half, since on a shared one a warp would wait for a phase without
@@ -26,9 +25,6 @@ class PagedModel(Model):
             self.B[("RE", u)] = Bar(DW // 2)
             for half in range(2):
                 self.B[("RF", u, half)] = Bar(1)
-        for i in range(2):
-            self.B[("VR", i)] = Bar(DW)
-            self.B[("VF", i)] = Bar(1)
 
 
 def roles_of(m, drop=None, shift=None, shared_full=False):
@@ -63,9 +59,10 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
         n = 0
         for typ, blk in units:
             for half in range(2):
+                if n + half >= nu:
+                    yield from wait("ring_empty", ("RE", (n + half) % nu), (n + half) // nu - 1)
+            for half in range(2):
                 slot = n % nu
-                if n >= nu:
-                    yield from wait("ring_empty", ("RE", slot), n // nu - 1)
                 yield ("expect_tx", full(n)[0])
                 yield ("copy", full(n)[0], lambda slot=slot, v=(typ, blk, half): m.write(
                     ("ring", slot), v, lambda p: {("dec", w) for w in range(4 * p[2], 4 * p[2] + 4)}))
@@ -86,15 +83,17 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
         for typ, blk in units:
             slot, x = n % nu, count[typ]
             yield from wait("ring_full", *full(n))
-            if x >= 2:
-                name = "k_free" if typ == "K" else "v_free"
-                yield from wait(name, (("KF" if typ == "K" else "VF"), x & 1), (x >> 1) - 1)
+            if typ == "K" and x >= 2:
+                yield from wait("k_free", ("KF", x & 1), (x >> 1) - 1)
+            if typ == "V" and x >= 1:
+                yield from wait("v_free", "VF", x - 1)
+            buf = x & 1 if typ == "K" else 0
             readers = ((lambda p: {("qk", t, p) for t in range(tiles[p])}) if typ == "K"
                        else (lambda p: {("pv", t, p) for t in range(tiles[p])}))
-            yield ("do", lambda slot=slot, v=(typ, blk, half), readers=readers: (
+            yield ("do", lambda slot=slot, v=(typ, blk, half), readers=readers, buf=buf: (
                 m.read(("ring", slot), v, ("dec", w)),
-                m.write((v[0], v[1] & 1, w), v[1], readers)))
-            yield ("arrive", (("KR" if typ == "K" else "VR"), x & 1))
+                m.write((v[0], buf, w), v[1], readers)))
+            yield ("arrive", ("KR", buf) if typ == "K" else "VR")
             yield ("arrive", ("RE", slot))
             n += 2
             count[typ] += 1
@@ -112,7 +111,7 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
             for w in range(RW):
                 m.read(("P", t, w), k, ("pv", t, k))
             for w in range(DW):
-                m.read(("V", k & 1, w), k, ("pv", t, k))
+                m.read(("V", 0, w), k, ("pv", t, k))
             m.reads.setdefault(("S", t), set()).add(("pv", t, k))
             for w in range(RW):
                 o = ("O", t, w)
@@ -148,7 +147,7 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
         for k in range(nb):
             nxt = k + 1 < nb
             boundary = nxt and blocks[k + 1][1]
-            yield from wait("v_ready", ("VR", k & 1), k >> 1)
+            yield from wait("v_ready", "VR", k)
             yield from product(0, k)
             if nxt and not boundary:
                 yield from wait("k_ready", ("KR", (k + 1) & 1), (k + 1) >> 1)
@@ -156,7 +155,7 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
                 yield from qk(0, k + 1)
             if tiles[k] == 2:
                 yield from product(1, k)
-            yield ("commit", ("VF", k & 1))
+            yield ("commit", "VF")
             if nxt:
                 if boundary:
                     yield from wait("q_ready", "QR", sq)
