@@ -19,11 +19,12 @@
 // through 0 * inf, so its token's scale is taken as zero in the tile and the
 // token is remembered: rows that do see it become NaN at the segment's end.
 //
-// The softmax reads S once.  Its reference maximum is lazy: it moves, and O and z are rescaled,
+// The softmax reads S twice (its maximum, then p): a read of 32 columns takes
+// about 70 cycles, a vote and a branch per 32 columns in a single pass took four
+// times that.  Its reference maximum is lazy: it moves, and O and z are rescaled,
 // only when a block's maximum outruns it by more than 8 in log2 units.  Any
 // reference that never falls more than that below the running maximum gives
-// the same u / z in exact arithmetic.  (Where it moves within a block, the p
-// already written are rescaled in place, which rounds them once more.)
+// the same u / z in exact arithmetic.
 //
 // Warp roles (20 warps, 96 registers each):
 //   0        producer: two lanes copy 32 keys each (codes and scales) of half a
@@ -238,20 +239,19 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
   }
 }
 
-// Maximum (kMin: minimum) of 32 raw scores held in registers.
-template <bool kMin>
-__device__ __forceinline__ float row_extreme(const uint32_t (&sr)[32]) {
+// Maximum of 64 raw scores held in registers, as eight independent chains of
+// three-input operations.
+__device__ __forceinline__ float row_max(const uint32_t (&sr)[64]) {
   auto f = [](uint32_t x) { return __uint_as_float(x); };
-  auto op3 = [](float a, float b, float c) { return kMin ? min3(a, b, c) : max3(a, b, c); };
-  float acc[4];
+  float acc[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    acc[j] = op3(f(sr[j]), f(sr[4 + j]), f(sr[8 + j]));
-    acc[j] = op3(acc[j], f(sr[12 + j]), f(sr[16 + j]));
-    acc[j] = op3(acc[j], f(sr[20 + j]), f(sr[24 + j]));
+  for (int j = 0; j < 8; ++j) {
+    acc[j] = max3(f(sr[j]), f(sr[8 + j]), f(sr[16 + j]));
+    acc[j] = max3(acc[j], f(sr[24 + j]), f(sr[32 + j]));
+    acc[j] = max3(acc[j], f(sr[40 + j]), f(sr[48 + j]));
+    acc[j] = fmaxf(acc[j], f(sr[56 + j]));
   }
-  const float a = op3(acc[0], acc[1], f(sr[28])), b = op3(acc[2], acc[3], f(sr[29]));
-  return op3(op3(a, b, f(sr[30])), f(sr[31]), f(sr[31]));
+  return max3(max3(acc[0], acc[1], acc[2]), max3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
 }
 
 // After a time-out: waits (100 ms at most) for a copy that is still in flight.
@@ -592,82 +592,97 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (walk.tiles(c) <= tile) continue;
         wait_bar(bar(S_FULL + tile), k & 1u, p.err, abort_flag);
         tc_fence_after();
-        // One pass over S, 32 columns at a time: the columns' maximum, the
-        // reference if it has to move, p = exp2(s * qscale - m_ref) as bf16 over
-        // the columns already read.
-        const int nv = min(kBT, lim - c.j * kBT);
-        u64 z2 = 0ull;
+        const int nv = min(kBT, lim - c.j * kBT);         // columns the row sees
+        const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
+        // the row's extreme over the columns it sees
+        float mb;
+        if (plain) {
+          float mx = -INFINITY;
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          const int left = nv - 32 * cc;                  // columns of these that the row sees
-          if (__all_sync(0xffffffffu, left <= 0)) {
-            uint32_t zero[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) zero[e] = 0u;
-            KVQ_ST16(s_col + 16u * cc, zero);
-            continue;
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t sr[64];
+            KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
+            KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+            tmem_wait_ld();
+            mx = fmaxf(mx, row_max(sr));
           }
-          uint32_t sr[32];
-          KVQ_LD32(sr, s_col + 32u * cc);
-          tmem_wait_ld();
-          const bool whole = __all_sync(0xffffffffu, left >= 32);
-          if (!whole) {
-            const uint32_t fill = __float_as_uint(neg ? INFINITY : -INFINITY);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e >= left) sr[e] = fill;
-          }
-          const float mx = neg ? row_extreme<true>(sr) : row_extreme<false>(sr);
-          const float mb = left > 0 ? mx * p.qscale : -INFINITY;
-          const bool need = mb > m_ref + kLazy;
-          if (__any_sync(0xffffffffu, need)) {
-            const float a = need ? ex2(m_ref - mb) : 1.f;  // 0 where the row had no key
-            if (need) m_ref = mb;
-            z *= a;
-            z2 = mul2(z2, pack2(a, a));
-            if (!c.start) {
+          mb = mx * p.qscale;
+        } else {
+          float mx = neg ? INFINITY : -INFINITY;
 #pragma unroll 1
-              for (int oc = 0; oc < D / 16; ++oc) {
-                uint32_t orr[16];
-                KVQ_LD16(orr, o_col + 16u * oc);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
-                KVQ_ST16(o_col + 16u * oc, orr);
-              }
-            }
-#pragma unroll 1
-            for (int pc = 0; pc < cc; ++pc) {              // the block's p so far
-              uint32_t pk[16];
-              KVQ_LD16(pk, s_col + 16u * pc);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                pk[e] = pack_bf16(__uint_as_float(pk[e] << 16) * a, __uint_as_float(pk[e] & 0xFFFF0000u) * a);
-              KVQ_ST16(s_col + 16u * pc, pk);
-            }
-          }
-          const u64 qs2 = pack2(p.qscale, p.qscale), nm2 = pack2(-m_ref, -m_ref);
-          uint32_t pk[16];
-          if (whole) {
+          for (int cc = 0; cc < 8; ++cc) {
+            uint32_t sr[16];
+            KVQ_LD16(sr, s_col + 16u * cc);
+            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
+              const float x = __uint_as_float(sr[e]);
+              if (16 * cc + e < nv) mx = neg ? fminf(mx, x) : fmaxf(mx, x);
+            }
+          }
+          mb = nv > 0 ? mx * p.qscale : -INFINITY;        // (none seen: never a new reference)
+        }
+        const bool need = mb > m_ref + kLazy;
+        if (__any_sync(0xffffffffu, need)) {
+          const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
+          if (need) m_ref = mb;
+          z *= a;
+          if (!c.start) {
+#pragma unroll 1
+            for (int oc = 0; oc < D / 16; ++oc) {
+              uint32_t orr[16];
+              KVQ_LD16(orr, o_col + 16u * oc);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+              KVQ_ST16(o_col + 16u * oc, orr);
+            }
+          }
+        }
+        // p = exp2(s * qscale - m_ref) as bf16 over the columns already read,
+        // 16 at a time, the next ones on their way
+        const u64 qs2 = pack2(p.qscale, p.qscale), nm2 = pack2(-m_ref, -m_ref);
+        u64 z2 = 0ull;
+        if (plain) {
+          uint32_t s0[16], s1[16];
+          auto columns = [&](const uint32_t (&sr)[16], int cc) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
               const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
               const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
               z2 = add2(z2, pack2(p0, p1));
               pk[e] = pack_bf16(p0, p1);
             }
-          } else {
+            KVQ_ST8(s_col + 8u * cc, pk);
+          };
+          KVQ_LD16(s0, s_col);
+#pragma unroll 1
+          for (int cc = 0; cc < 8; cc += 2) {
+            tmem_wait_ld();
+            KVQ_LD16(s1, s_col + 16u * cc + 16u);
+            columns(s0, cc);
+            tmem_wait_ld();
+            if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
+            columns(s1, cc + 1);
+          }
+        } else {
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            const int left = nv - 16 * cc;
+            uint32_t sr[16], pk[8];
+            KVQ_LD16(sr, s_col + 16u * cc);
+            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
               const float p0 = 2 * e < left ? ex2(lo_f(x)) : 0.f;
               const float p1 = 2 * e + 1 < left ? ex2(hi_f(x)) : 0.f;
               z2 = add2(z2, pack2(p0, p1));
               pk[e] = pack_bf16(p0, p1);
             }
+            KVQ_ST8(s_col + 8u * cc, pk);
           }
-          KVQ_ST16(s_col + 16u * cc, pk);
         }
         z += lo_f(z2) + hi_f(z2);
         tmem_wait_st();
