@@ -29,6 +29,8 @@
 // "Block KV decoding: less workspace, more time"
 // (huhohoo.com/en/docs/llm/kv-block-decode-cost, section "Do not average
 // independently normalized blocks").
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "paged.cuh"
 
@@ -121,6 +123,13 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w) {
   return r;
 }
 
+// Nibble 0 of each half without a shift, as 128 + n.
+__device__ __forceinline__ uint32_t nibbles_low(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(0x000F000Fu), "n"(0x43004300u));
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // layout of one warp's shared memory
 // ---------------------------------------------------------------------------
@@ -166,6 +175,7 @@ template <int BITS, int D, int NT, int NS>
 struct Pos {
   // a place in the worker's list of blocks
   int i, h, j, nb;
+  int pi, at;                     // its page's index in the sequence, its first row there
   long long left;                 // blocks from here to the worker's end
   Item it;
   SeqView s;
@@ -203,8 +213,14 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
   };
   auto advance = [&](Place& a) {               // the next block; true where a new segment begins
     if (--a.left == 0) return false;
-    if (++a.j < a.nb) return false;
-    a.j = 0;
+    if (++a.j < a.nb) {
+      if ((a.at += kBT) == P) {                // (a page holds whole blocks)
+        a.at = 0;
+        ++a.pi;
+      }
+      return false;
+    }
+    a.j = a.pi = a.at = 0;
     if (++a.h == H) {
       a.h = 0;
       do ++a.i;
@@ -221,18 +237,19 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
     cur.h = static_cast<int>(off / cur.nb);
     cur.j = static_cast<int>(off % cur.nb);
     cur.left = wr.g1 - wr.g0;
+    cur.pi = cur.j * kBT / P;
+    cur.at = cur.j * kBT - cur.pi * P;
   }
 
   // ---- block copies -------------------------------------------------------
   // a lane's destination offsets are the same for every block
   auto page_of = [&](const Place& a) {
-    return __ldg(p.t.table + static_cast<long long>(a.it.b) * p.t.max_pages + a.j * kBT / P);
+    return __ldg(p.t.table + static_cast<long long>(a.it.b) * p.t.max_pages + a.pi);
   };
   auto copy = [&](const Place& a, int page, uint32_t dst) {
     page = read_page(page, p.t.pages, p.err);
     const long long head = static_cast<long long>(page) * H + a.h;
-    const int at = a.j * kBT % P;
-    const long long tok = head * P + at;                     // the page's arrays are dense: token rows of all heads
+    const long long tok = head * P + a.at;                     // the page's arrays are dense: token rows of all heads
     const uint8_t* kc = p.k_codes + tok * C::RB + lane * 16;
     const uint8_t* vc = p.v_codes + tok * C::RB + lane * 16;
 #pragma unroll
@@ -469,7 +486,9 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
     }
 
     // ---- softmax --------------------------------------------------------------
-    const bool masked = t0 + kBT > full;
+    // (two bodies: only an item's last blocks pay for the selections)
+    auto softmax_pv = [&](auto masked_c) {
+    constexpr bool masked = decltype(masked_c)::value;
     bool need = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -547,9 +566,9 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
                        : "=r"(xr[0]), "=r"(xr[1])
                        : "r"(st_u + C::kOffV + 16 * v_slot<C::CH>(tr, fg))
                        : "memory");
-          const uint32_t off = 0xC1B8C1B8u;                   // -23
-          const uint32_t a0[4] = {add_bf16x2(nibbles<0, false>(xr[0]), off), add_bf16x2(nibbles<1, false>(xr[0]), off),
-                                  add_bf16x2(nibbles<0, false>(xr[1]), off), add_bf16x2(nibbles<1, false>(xr[1]), off)};
+          const uint32_t off = 0xC1B8C1B8u, off0 = 0xC307C307u;   // -23, -135
+          const uint32_t a0[4] = {add_bf16x2(nibbles_low(xr[0]), off0), add_bf16x2(nibbles<1, false>(xr[0]), off),
+                                  add_bf16x2(nibbles_low(xr[1]), off0), add_bf16x2(nibbles<1, false>(xr[1]), off)};
           const uint32_t a1[4] = {add_bf16x2(nibbles<2, false>(xr[0]), off), add_bf16x2(nibbles<3, false>(xr[0]), off),
                                   add_bf16x2(nibbles<2, false>(xr[1]), off), add_bf16x2(nibbles<3, false>(xr[1]), off)};
 #pragma unroll
@@ -561,12 +580,12 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
             }
         } else {
           ldsm4t(xr, st_u + C::kOffV + 16 * v_slot<C::CH>(tr, 2 * fg + (lane >> 4)));
-          const uint32_t ol = 0xC1F8C1F8u, oh = 0xC3B8C3B8u;   // -31, -368
+          const uint32_t ol = 0xC1F8C1F8u, ol0 = 0xC30FC30Fu, oh = 0xC3B8C3B8u;   // -31, -143, -368
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t xa = xr[2 * k], xb = xr[2 * k + 1];
-            const uint32_t a0[4] = {add_bf16x2(nibbles<0, false>(xa), ol), add_bf16x2(nibbles<2, false>(xa), ol),
-                                    add_bf16x2(nibbles<0, false>(xb), ol), add_bf16x2(nibbles<2, false>(xb), ol)};
+            const uint32_t a0[4] = {add_bf16x2(nibbles_low(xa), ol0), add_bf16x2(nibbles<2, false>(xa), ol),
+                                    add_bf16x2(nibbles_low(xb), ol0), add_bf16x2(nibbles<2, false>(xb), ol)};
             const uint32_t a1[4] = {add_bf16x2(nibbles<1, true>(xa), oh), add_bf16x2(nibbles<3, true>(xa), oh),
                                     add_bf16x2(nibbles<1, true>(xb), oh), add_bf16x2(nibbles<3, true>(xb), oh)};
 #pragma unroll
@@ -580,6 +599,9 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
         }
       }
     }
+    };
+    if (t0 + kBT > full) softmax_pv(std::true_type{});
+    else softmax_pv(std::false_type{});
     __syncwarp();                               // the stage may be overwritten
 
     // ---- end of a segment -------------------------------------------------------
