@@ -17,14 +17,17 @@ struct RowRange {
   int r0, n;
   bool bad;
 };
-__device__ __forceinline__ RowRange row_range(const int32_t* cu, int b, int T, int max_rows) {
-  const int c0 = __ldcg(cu + b), c1 = __ldcg(cu + b + 1);
+__device__ __forceinline__ RowRange row_range(int c0, int c1, int T, int max_rows) {
   RowRange r;
   r.r0 = min(max(c0, 0), T);
   const int r1 = min(max(c1, r.r0), T);
   r.n = min(r1 - r.r0, max_rows);
   r.bad = c0 != r.r0 || c1 != r1 || r.n != r1 - r.r0;
   return r;
+}
+
+__device__ __forceinline__ RowRange row_range(const int32_t* cu, int b, int T, int max_rows) {
+  return row_range(__ldcg(cu + b), __ldcg(cu + b + 1), T, max_rows);
 }
 
 // Page number of a block-table entry for reading: one outside the pool is

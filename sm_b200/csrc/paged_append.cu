@@ -33,29 +33,57 @@ struct GroupSize {
   int g, lg;                       // lg: its logarithm where it is a power of two, else -1
   __device__ __forceinline__ int div(int x) const { return lg >= 0 ? x >> lg : x / g; }
 };
-__device__ __forceinline__ long long unit_base(const int32_t* cu, int b, int T, const GroupSize& gs) {
-  return gs.div(min(max(__ldcg(cu + b), 0), T)) + 2LL * b;
+__device__ __forceinline__ long long unit_base(int c, int b, int T, const GroupSize& gs) {
+  return gs.div(min(max(c, 0), T)) + 2LL * b;
 }
 // The same for rows: base(b) = cu[b].
-__device__ __forceinline__ long long row_base(const int32_t* cu, int b, int T) {
-  return min(max(__ldcg(cu + b), 0), T);
-}
+__device__ __forceinline__ long long row_base(int c, int T) { return min(max(c, 0), T); }
 
-// Largest b in [0, S) with base(b) <= u, by one warp, 32 probes a round.
+// The sequence of unit u: the largest b in [0, S) with base(cu[b], b) <= u (0
+// if none), with cu[b] and cu[b + 1], by one warp.  Up to 127 sequences take one
+// round of loads, four entries a lane; more take one per factor of 32.
+struct Found {
+  int b, c0, c1;
+};
 template <typename Base>
-__device__ __forceinline__ int warp_find(int S, long long u, Base base) {
+__device__ __forceinline__ Found warp_find(const int32_t* cu, int S, long long u, Base base) {
   const int lane = threadIdx.x & 31;
+  Found f;
+  if (S < 128) {
+    int c[4], count = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = lane + 32 * k;
+      c[k] = i <= S ? __ldcg(cu + i) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = lane + 32 * k;
+      count += __popc(__ballot_sync(0xffffffffu, i < S && base(c[k], i) <= u));
+    }
+    f.b = max(count - 1, 0);
+    auto entry = [&](int i) {
+      const int k = i >> 5;
+      return __shfl_sync(0xffffffffu, k == 0 ? c[0] : k == 1 ? c[1] : k == 2 ? c[2] : c[3], i & 31);
+    };
+    f.c0 = entry(f.b);
+    f.c1 = entry(f.b + 1);
+    return f;
+  }
   int lo = 0, n = S;
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int at = lane * step;
-    const bool le = at < n && base(lo + at) <= u;
+    const bool le = at < n && base(__ldcg(cu + lo + at), lo + at) <= u;
     const int k = __popc(__ballot_sync(0xffffffffu, le));
-    if (k == 0) return lo;
+    if (k == 0) break;
     lo += (k - 1) * step;
     n = min(step, n - (k - 1) * step);
   }
-  return lo;
+  f.b = lo;
+  f.c0 = __ldcg(cu + lo);
+  f.c1 = __ldcg(cu + lo + 1);
+  return f;
 }
 
 struct AppendParams {
@@ -282,9 +310,28 @@ struct GroupAt {
   int tok0, first, len, row0;
 };
 
+// A lane's eight features of a V row, given its group's maximum, or its scale.
+__device__ __forceinline__ void store_v_scaled(const AppendParams& p, long long head, long long tok, int d0,
+                                               const Eight& x, float sc) {
+  const float rs = __frcp_rn(sc);
+  if ((d0 & (p.group - 1)) == 0) p.v_scales[head * p.v_scales_head + tok * (p.D >> p.lg) + (d0 >> p.lg)] = sc;
+  Eight s8, r8;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    s8.v[k] = pack2(sc, sc);
+    r8.v[k] = pack2(rs, rs);
+  }
+  quantize8(p.v_codes + head * p.v_codes_head, tok * p.D + d0, x, s8, r8, p.bits,
+            plain_scale(sc) && finite2(sum4(x)));
+}
+__device__ __forceinline__ void store_v_row(const AppendParams& p, long long head, long long tok, int d0,
+                                            const Eight& x, float top) {
+  store_v_scaled(p, head, tok, d0, x, group_scale(top, p.bits == 4 ? 7 : 127));
+}
+
 template <bool kBf16, int LPR, int PASS>
 __device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max, int h, const GroupAt& a,
-                                             const int32_t* table, float* tail) {
+                                             const int32_t* table, float* tail, bool with_v) {
   constexpr int RPP = kThreads / LPR;              // rows of a pass
   const int g = p.group, D = p.D;
   const int qmax = p.bits == 4 ? 7 : 127;
@@ -303,11 +350,37 @@ __device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max
       else x[q] = load8<kBf16>(p.K, (a.row0 + a.tok0 + r - a.first) * p.k_stride + static_cast<long long>(h) * D + d0);
     }
   }
+  // a call of one token a sequence: its V row is the same CTA's
+  const bool v_on = with_v && on && slot == 0;
+  Eight v = zero8();
+  if (v_on) v = load8<kBf16>(p.V, (a.row0 + a.tok0 + kept - a.first) * p.v_stride + static_cast<long long>(h) * D + d0);
   if (p.rot > 0) {
     const int half = p.rot / 2;
     const bool turns = on && d0 < p.rot, upper = !p.interleaved && d0 >= half;
     const int lane = threadIdx.x & 31;
     const int partner = p.interleaved || !turns ? lane : (upper ? lane - half / 8 : lane + half / 8);
+    // a pair's first feature becomes x c - y s, its second y c + x s
+    Eight c, s;
+    auto angles = [&](int pos) {
+      const float* tab = p.rope + static_cast<long long>(pos) * p.rot;
+      if (p.interleaved) {
+        const float4 cv = __ldg(reinterpret_cast<const float4*>(tab + d0 / 2));
+        const float4 sv = __ldg(reinterpret_cast<const float4*>(tab + half + d0 / 2));
+        const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          c.v[k] = pack2(cc[k], cc[k]);
+          s.v[k] = pack2(ss[k], ss[k]);
+        }
+      } else {
+        const int e = upper ? d0 - half : d0;
+        c = load8f(tab + e);
+        s = load8f(tab + half + e);
+      }
+    };
+    // the thread's first new row's are asked for before its rows are waited for
+    const int q_first = max(0, (kept - slot + RPP - 1) / RPP);
+    if (turns && a.tok0 + q_first * RPP + slot < min(a.len, p.n_pos)) angles(a.tok0 + q_first * RPP + slot);
 #pragma unroll
     for (int q = 0; q < PASS; ++q) {
       const int r = q * RPP + slot, pos = a.tok0 + r;
@@ -318,32 +391,17 @@ __device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max
       for (int k = 0; k < 4; ++k)
         o.v[k] = p.interleaved ? (x[q].v[k] << 32 | x[q].v[k] >> 32) : __shfl_sync(0xffffffffu, x[q].v[k], partner);
       if (turn) {
-        // a pair's first feature becomes x c - y s, its second y c + x s
-        const float* tab = p.rope + static_cast<long long>(pos) * p.rot;
-        Eight c, s;
-        if (p.interleaved) {
-          const float4 cv = __ldg(reinterpret_cast<const float4*>(tab + d0 / 2));
-          const float4 sv = __ldg(reinterpret_cast<const float4*>(tab + half + d0 / 2));
-          const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            c.v[k] = pack2(cc[k], cc[k]);
-            s.v[k] = pack2(-ss[k], ss[k]);
-          }
-        } else {
-          const int e = upper ? d0 - half : d0;
-          c = load8f(tab + e);
-          s = load8f(tab + half + e);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s.v[k] = upper ? s.v[k] : neg2(s.v[k]);
-        }
+        if (q != q_first) angles(pos);
+        const u64 flip = p.interleaved ? 0x0000000080000000ull : (upper ? 0ull : 0x8000000080000000ull);
         // (-s) y added is s y subtracted, bit for bit; scalar operations, since
         // a packed product and sum may become one rounding
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          x[q].v[k] = pack2(__fadd_rn(__fmul_rn(x[q].at(2 * k), c.at(2 * k)), __fmul_rn(o.at(2 * k), s.at(2 * k))),
+        for (int k = 0; k < 4; ++k) {
+          const u64 sk = s.v[k] ^ flip;
+          x[q].v[k] = pack2(__fadd_rn(__fmul_rn(x[q].at(2 * k), c.at(2 * k)), __fmul_rn(o.at(2 * k), lo_f(sk))),
                             __fadd_rn(__fmul_rn(x[q].at(2 * k + 1), c.at(2 * k + 1)),
-                                      __fmul_rn(o.at(2 * k + 1), s.at(2 * k + 1))));
+                                      __fmul_rn(o.at(2 * k + 1), hi_f(sk))));
+        }
       }
     }
   }
@@ -357,6 +415,15 @@ __device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max
   if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
     if (threadIdx.x == 0) record_error(p.err, KVQ_ERR_INDEX);
     return;
+  }
+  const long long head = static_cast<long long>(page) * p.H + h;
+  const int in_page = a.tok0 % p.P;
+  if (with_v && threadIdx.x < 32) {                // (the row's lanes are the warp's first)
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v.at(k)));
+    for (int o = 1; o < g >> 3; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (v_on) store_v_row(p, head, in_page + kept, d0, v, m);
   }
   // a channel's maximum over the group's rows
   float top[8];
@@ -374,8 +441,6 @@ __device__ __forceinline__ void append_k_vec(const AppendParams& p, float* s_max
   }
   __syncthreads();
   // a thread turns one channel's maximum into its scale (D <= 256: two a thread)
-  const long long head = static_cast<long long>(page) * p.H + h;
-  const int in_page = a.tok0 % p.P;
   float* s_scale = s_max + 4 * D;                  // [D], then the reciprocals
   for (int d = threadIdx.x; d < D; d += kThreads) {
     const float m = fmaxf(fmaxf(s_max[d], s_max[D + d]), fmaxf(s_max[2 * D + d], s_max[3 * D + d]));
@@ -442,19 +507,7 @@ __device__ __forceinline__ void append_v_vec(const AppendParams& p, int h, const
     const int r = q * RPP + slot;
     const float sc = lanes >= PASS ? __shfl_sync(0xffffffffu, scale, (threadIdx.x & 31) - own + q)
                                    : group_scale(mx[q], qmax);
-    if (on && r >= kept && r < live) {
-      const float rs = __frcp_rn(sc);
-      const long long tok = in_page + r;
-      if (own == 0) p.v_scales[head * p.v_scales_head + tok * (D >> p.lg) + (d0 >> p.lg)] = sc;
-      Eight s8, r8;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s8.v[k] = pack2(sc, sc);
-        r8.v[k] = pack2(rs, rs);
-      }
-      quantize8(p.v_codes + head * p.v_codes_head, tok * D + d0, x[q], s8, r8, p.bits,
-                plain_scale(sc) && finite2(sum4(x[q])));
-    }
+    if (on && r >= kept && r < live) store_v_scaled(p, head, in_page + r, d0, x[q], sc);
   }
 }
 
@@ -468,13 +521,18 @@ __global__ void __launch_bounds__(kThreads, LPR == 0 || PASS == 8 ? 3 : 6) paged
   const int h = blockIdx.y, g = p.group;
   const bool v_part = blockIdx.z != 0;              // K has a CTA of its own (LPR > 0)
   const GroupSize gs{g, LPR > 0 ? max(p.lg, 0) : p.lg};       // (the vector form's groups are powers of two)
-  const int b = p.max_new == 1 ? static_cast<int>(u)
-                               : warp_find(p.S, u, [&](int i) { return unit_base(p.cu, i, p.T, gs); });
-  // one round of loads
-  const int c0 = __ldcg(p.cu + b), len = __ldg(p.lengths + b);
-  const RowRange rr = row_range(p.cu, b, p.T, p.max_new);
-  const int slot = p.slots ? __ldg(p.slots + b) : b;
-  const int j = p.max_new == 1 ? 0 : static_cast<int>(u - (gs.div(min(max(c0, 0), p.T)) + 2LL * b));
+  const bool single = p.max_new == 1;
+  Found f{static_cast<int>(u), 0, 0};
+  if (single) {
+    f.c0 = __ldcg(p.cu + f.b);
+    f.c1 = __ldcg(p.cu + f.b + 1);
+  } else {
+    f = warp_find(p.cu, p.S, u, [&](int c, int i) { return unit_base(c, i, p.T, gs); });
+  }
+  const int b = f.b;
+  const int len = __ldg(p.lengths + b), slot = p.slots ? __ldg(p.slots + b) : b;
+  const RowRange rr = row_range(f.c0, f.c1, p.T, p.max_new);
+  const int j = single ? 0 : static_cast<int>(u - unit_base(f.c0, b, p.T, gs));
   if (j < 0) return;                                // before the first sequence's rows
   const bool report = threadIdx.x == 0 && j == 0 && h == 0 && !v_part;
   if (rr.bad && report) record_error(p.err, KVQ_ERR_LENGTH);
@@ -511,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, LPR == 0 || PASS == 8 ? 3 : 6) paged
       }
       append_group<kBf16>(p, s_x, h, at.tok0, first, len, rr.r0, page, tail);
     } else {
-      append_k_vec<kBf16, LPR, PASS>(p, s_x, h, at, table, tail);
+      append_k_vec<kBf16, LPR, PASS>(p, s_x, h, at, table, tail, single);
       __syncthreads();                              // the tail rows were read, the shared maxima too
     }
   }
@@ -579,8 +637,9 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(GatherPara
     const long long row = row0 + warp;
     int page = -1, at = -1;                         // at < 0: a zero row; page < 0: no sequence's row
     if (row < p.T) {
-      const int b = warp_find(p.S, row, [&](int i) { return row_base(p.cu, i, p.T); });
-      const RowRange rr = row_range(p.cu, b, p.T, p.max_rows);
+      const Found f = warp_find(p.cu, p.S, row, [&](int c, int) { return row_base(c, p.T); });
+      const int b = f.b;
+      const RowRange rr = row_range(f.c0, f.c1, p.T, p.max_rows);
       if (lane == 0 && rr.bad) record_error(p.err, KVQ_ERR_LENGTH);
       if (row >= rr.r0 && row < rr.r0 + rr.n) {
         const int start = __ldg(p.starts + b);
@@ -716,7 +775,7 @@ kvq_status launch_append(const AppendCall& a, cudaStream_t s) {
   if (units > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   void (*kernel)(AppendParams) = nullptr;
   size_t smem = 6 * static_cast<size_t>(a.g.D) * sizeof(float);
-  unsigned parts = 2;                               // K and V
+  unsigned parts = a.max_new == 1 ? 1 : 2;          // K and V, or (one token a sequence) both in one CTA
   int pass = 0, lpr = 8;
   if (vector_form(a)) {
     while (8 * lpr < a.g.D) lpr *= 2;
