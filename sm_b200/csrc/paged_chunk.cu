@@ -61,6 +61,24 @@ constexpr float kLazy = 8.f;
 constexpr int kTileHalf = kBT * 128;              // 16 KB: 128 rows x 64 bf16
 constexpr int kMaxUnits = 12;                    // half-units of the ring
 
+// Powers of two that keep the fp16 tiles in range.  The tiles hold (code - qmax)
+// * scale * 2^(kTop - e), below 2^15 (the scale is below 2^(e + 1), the code at
+// most 2^7 away from zero), where e is the exponent of the largest K (V) scale of
+// the sequence and KV head; a query row is multiplied by 2^(kTopQ - e) of its own.
+// Nothing but the powers changes with what is far away or behind a row's position:
+// the bits do not, short of values 2^21 below the largest scale, where fp16 loses
+// precision.
+constexpr int kTop = 7, kTopQ = 14;
+constexpr float kTopP = 7.f;                     // p <= 2^(kTopP + kLazy) = 2^15
+constexpr int kExpMin = -100, kExpMax = 127;
+constexpr int kParts = 16;                       // of a sequence's groups, each with a maximum of its own
+
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// exponent of a value given by its bits
+__device__ __forceinline__ int exponent(uint32_t bits) {
+  return min(max(static_cast<int>(bits >> 23) - 127, kExpMin), kExpMax);
+}
+
 template <int D>
 struct Smem {
   static constexpr int kTile = D / 64 * kTileHalf;
@@ -68,10 +86,11 @@ struct Smem {
   static constexpr int kK = 2 * kTile;             // two K tiles
   static constexpr int kV = kK + 2 * kTile;        // one V tile
   static constexpr int kRing = kV + kTile;
-  static constexpr int kRingBytes = 59 * 1024;
+  static constexpr int kRingBytes = 55 * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 50 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
-  static constexpr int kPre = kMisc + 80;          // int pre[S + 1] (inline plan)
+  static constexpr int kMisc = kBar + 58 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kPow = kMisc + 80;          // int2 [4]: a segment's exponents (K, V)
+  static constexpr int kPre = kPow + 32;            // int pre[S + 1] (inline plan)
 };
 
 enum Bar {
@@ -84,8 +103,10 @@ enum Bar {
   S_FULL = 42,                   // [2]
   P_FULL = 44,                   // [2]
   PV_DONE = 46,                  // [2]
-  Q_READY = 48,
-  Q_FREE = 49,
+  Q_READY = 48,                  // [2]
+  Q_FP16 = 50,                   // [2]
+  Q_FREE = 52,
+  POWERS = 53,                   // [4]
 };
 
 struct Params {
@@ -95,6 +116,7 @@ struct Params {
   const float* k_scales;
   const uint8_t* v_codes;
   const float* v_scales;
+  const uint32_t* tops;          // [S][H][2][kParts]: bits of the largest K and V scales
   float qscale;                  // scale * log2(e)
   __nv_bfloat16* O;
   float* partials;               // [2 ctas][8][D + 2][32]
@@ -162,7 +184,8 @@ struct Walk {
 // two tokens, whose rows swizzle differently.
 template <int BITS, int D, bool kV>
 __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned char* dst, int wk, int lane, int nv,
-                                            int t_base, unsigned long long seg_key, unsigned long long* s_bad) {
+                                            float power, int t_base, unsigned long long seg_key,
+                                            unsigned long long* s_bad) {
   constexpr int kCb = D * BITS / 8, QN = D / 16, TPP = 32 / QN;
   const int q = lane % QN, tt = lane / QN;
   const bool swap = D == 128 && (q & 4) != 0;
@@ -181,6 +204,8 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
         ks[4 * i + 2] = pack2(v1.x, v1.y);
         ks[4 * i + 3] = pack2(v1.z, v1.w);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ks[i] = mul2(ks[i], pack2(power, power));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) ks[i] = 0ull;
@@ -199,6 +224,7 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
           atomicMax(s_bad, seg_key | static_cast<unsigned>(0x7fffffff - (t_base + t)));
           s = 0.f;
         }
+        s *= power;
         s2 = pack2(s, s);
       }
       uint32_t h[8];
@@ -211,7 +237,7 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
           for (int r = 0; r < 4; ++r) {
             const u64 f = fma2(nibble_pair(byte_at15(w[i], r)), mul, add);
             const u64 x = mul2(f, kV ? s2 : ks[4 * i + r]);
-            h[4 * i + r] = pack_bf16(lo_f(x), hi_f(x));
+            h[4 * i + r] = pack_f16(lo_f(x), hi_f(x));
           }
       } else {
         const uint4 w4 = *reinterpret_cast<const uint4*>(u + tu * kCb + 16 * q);
@@ -222,7 +248,7 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
           for (int r = 0; r < 4; r += 2) {
             const u64 f = add2(byte_pair(w[i], r), sub);
             const u64 x = mul2(f, kV ? s2 : ks[2 * i + r / 2]);
-            h[2 * i + r / 2] = pack_bf16(lo_f(x), hi_f(x));
+            h[2 * i + r / 2] = pack_f16(lo_f(x), hi_f(x));
           }
       }
       o[0] = make_uint4(h[0], h[1], h[2], h[3]);
@@ -254,10 +280,97 @@ __device__ __forceinline__ float row_max(const uint32_t (&sr)[64]) {
   return max3(max3(acc[0], acc[1], acc[2]), max3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
 }
 
+// A query row of a tile from bf16 to fp16, in place, with the power of two that
+// takes its largest element into [2^kTopQ, 2^(kTopQ + 1)); returns the inverse.
+template <int D>
+__device__ __forceinline__ float row_to_f16(unsigned char* tile, int r) {
+  auto chunk = [&](int ch) { return reinterpret_cast<uint4*>(tile + (ch >> 3) * kTileHalf + swz(r, ch & 7)); };
+  uint32_t m = 0;                                  // (magnitudes order as their bits do)
+#pragma unroll 2
+  for (int ch = 0; ch < D / 8; ++ch) {
+    const uint4 x = *chunk(ch);
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+  }
+  m = max(m & 0xffffu, m >> 16);
+  const int e = min(max(static_cast<int>(m >> 7) - 127, kExpMin), kExpMax);
+  const float f = exp2i(kTopQ - e);
+  auto turn = [&](uint32_t v) {
+    return pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+  };
+#pragma unroll 2
+  for (int ch = 0; ch < D / 8; ++ch) {
+    const uint4 x = *chunk(ch);
+    *chunk(ch) = make_uint4(turn(x.x), turn(x.y), turn(x.z), turn(x.w));
+  }
+  return exp2i(e - kTopQ);
+}
+
+// Bounded wait: after about two seconds raises the CTA's abort flag and goes on;
+// once the flag is up every later wait gives up too, and the CTA records
+// KVQ_ERR_TIMEOUT as it ends.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try(bar, parity)) return;
+  const uint32_t t0 = static_cast<uint32_t>(globaltimer());
+  uint32_t it = 0;
+  while (!mbar_try(bar, parity))
+    if ((++it & 15u) == 0) {
+      if (*abort_flag) return;
+      if (static_cast<uint32_t>(globaltimer()) - t0 > 2000000000u) *abort_flag = 1;
+    }
+}
+
 // After a time-out: waits (100 ms at most) for a copy that is still in flight.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try(bar, parity) && globaltimer() - t0 < 100000000ull) {
+  }
+}
+
+// The largest K and V scales of a sequence and KV head, in kParts parts of its
+// groups of 32 tokens: a warp a group, a CTA a part.  It reads the scales alone
+// (32 of 160 bytes a token at D = 128 and 4 bits), and the attention finds them
+// in the L2 afterwards.
+constexpr int kScanWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kScanWarps) paged_scales_kernel(Batch t, const float* k_scales,
+                                                                       const float* v_scales, uint32_t* tops,
+                                                                       unsigned int* err) {
+  griddep_wait();
+  const int b = blockIdx.x, h = blockIdx.y, part = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const SeqView s = seq_view(t, b);
+  const int32_t* table = t.table + static_cast<long long>(b) * t.max_pages;
+  uint32_t top[2] = {0u, 0u};
+  if (s.n > 0)
+#pragma unroll 4
+    for (int g = part * kScanWarps + warp; 32 * g < s.len; g += kParts * kScanWarps) {
+      const int pi = 32 * g / t.P;
+      const long long tok =
+          (static_cast<long long>(read_page(__ldg(table + pi), t.pages, err)) * t.H + h) * t.P + 32 * g - pi * t.P;
+      const float* at[2] = {k_scales + (tok >> 5) * D + lane * (D / 32), v_scales + (tok + lane) * (D / 32)};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        __align__(16) float x[D / 32];
+        if (D == 128) *reinterpret_cast<float4*>(x) = __ldg(reinterpret_cast<const float4*>(at[i]));
+        else *reinterpret_cast<float2*>(x) = __ldg(reinterpret_cast<const float2*>(at[i]));
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {                // (what is not finite stays that whatever the power)
+          const uint32_t v = __float_as_uint(x[e]) & 0x7fffffffu;
+          if (v < 0x7f800000u && (i == 0 || 32 * g + lane < s.len)) top[i] = max(top[i], v);
+        }
+      }
+    }
+  __shared__ uint32_t s_top[2][kScanWarps];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, top[i]);
+    if (lane == 0) s_top[i][warp] = m;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    uint32_t m = 0u;
+    for (int w = 0; w < kScanWarps; ++w) m = max(m, s_top[threadIdx.x][w]);
+    tops[((static_cast<long long>(b) * t.H + h) * 2 + threadIdx.x) * kParts + part] = m;
   }
 }
 
@@ -271,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   unsigned char* sm = smem_raw + (base - raw_addr);
   int* s_pre = reinterpret_cast<int*>(sm + M::kPre);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + M::kMisc + 4);
+  int2* s_pow = reinterpret_cast<int2*>(sm + M::kPow);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + M::kMisc + 8);
   const uint32_t bar0 = base + M::kBar;
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -297,10 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init(bar(S_FULL + i), 1);
       mbar_init(bar(P_FULL + i), 4);
       mbar_init(bar(PV_DONE + i), 1);
+      mbar_init(bar(Q_READY + i), 1);
+      mbar_init(bar(Q_FP16 + i), 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(bar(POWERS + i), 1);
     mbar_init(bar(V_READY), kDecodeWarps);
     mbar_init(bar(V_FREE), 1);
-    mbar_init(bar(Q_READY), 1);
     mbar_init(bar(Q_FREE), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -352,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       look();
       uint32_t n = 0, slot = half, wraps = 0;             // half-units issued; this half's slot and its rounds
       auto unit = [&](bool is_v, long long tok, int groups) {
-        if (lane < 4 && wraps > 0) wait_bar(bar(RING_EMPTY + slot), (wraps - 1) & 1u, p.err, abort_flag);
+        if (lane < 4 && wraps > 0) wait(bar(RING_EMPTY + slot), (wraps - 1) & 1u, abort_flag);
         if (__any_sync(0xffffffffu, *abort_flag)) return;   // after a time-out nothing more is copied
         const uint32_t fb = bar(RING_FULL + 2 * slot + half);
         if ((lane & ~2) == 0)                             // (a half past the end brings nothing)
@@ -374,26 +490,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       };
       long long tok_v = 0, tok = 0;
       int groups_v = 0, groups = 0;
-      int blocks = static_cast<int>(wr.g1 - wr.g0), k_left = blocks;
-      auto k_unit = [&]() {
-        tok_v = tok;
-        groups_v = groups;
-        tok = read_page(page, p.t.pages, p.err) * page_tokens + kc.h * head_tokens + at;
-        groups = (min(kBT, __shfl_sync(0xffffffffu, left, 0)) + 31) >> 5;
-        walk.next(kc);
-        look();
-        unit(false, tok, groups);
-        --k_left;
-      };
-      k_unit();
-      for (; blocks > 0; --blocks) {
-        if (k_left > 0) {
-          k_unit();
-        } else {
-          tok_v = tok;
-          groups_v = groups;
+      const int blocks = static_cast<int>(wr.g1 - wr.g0);
+#pragma unroll 1
+      for (int i = 0; i <= blocks; ++i) {
+#pragma unroll 1
+        for (int is_v = i == blocks; is_v < 2; ++is_v) {  // K(i), then V(i - 1)
+          if (!is_v) {
+            tok_v = tok;
+            groups_v = groups;
+            tok = read_page(page, p.t.pages, p.err) * page_tokens + kc.h * head_tokens + at;
+            groups = (min(kBT, __shfl_sync(0xffffffffu, left, 0)) + 31) >> 5;
+            walk.next(kc);
+            look();
+          } else if (i == 0) {
+            break;
+          } else if (i == blocks) {
+            tok_v = tok;
+            groups_v = groups;
+          }
+          unit(is_v, is_v ? tok_v : tok, is_v ? groups_v : groups);
         }
-        unit(true, tok_v, groups_v);
       }
       // The decode warps took every copy before they ended, unless a wait ran
       // out: then the last ones in flight are waited for here (again bounded),
@@ -413,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // there first, and 32 of them a block took longer than their execution.
       const uint32_t lead = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint32_t idesc_qk = instr_desc(kBT, false);
-      const uint32_t idesc_pv = instr_desc(D, true);
+      const uint32_t idesc_qk = instr_desc_f16(kBT, false);
+      const uint32_t idesc_pv = instr_desc_f16(D, true);
       // descriptors: the address field counts 16-byte units, so a step adds to the low word
       const uint64_t dq = smem_desc(base + M::kQ, 16, 1024), dk = smem_desc(base + M::kK, 16, 1024),
                      dv = smem_desc(base + M::kV, kTileHalf, 1024);
@@ -430,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       };
       uint32_t done[2] = {0, 0};                          // P V products issued per tile
       auto pv = [&](int t, bool first) {
-        wait_bar(bar(P_FULL + t), done[t] & 1u, p.err, abort_flag);
+        wait(bar(P_FULL + t), done[t] & 1u, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < kBT / 16; ++i)
@@ -442,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // S of a tile overwrites its P: the last P V product must be done
       auto pv_done = [&](int t) {
         if (done[t] > 0) {
-          wait_bar(bar(PV_DONE + t), (done[t] - 1) & 1u, p.err, abort_flag);
+          wait(bar(PV_DONE + t), (done[t] - 1) & 1u, abort_flag);
           tc_fence_after();
         }
       };
@@ -456,40 +572,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         walk.next(c);
         return __shfl_sync(0xffffffffu, f, 0);
       };
-      uint32_t fc = flags(), fn = flags();                // the current block's and the next one's
-      uint32_t sq = 0;
-      wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
-      ++sq;
-      wait_bar(bar(K_READY), 0u, p.err, abort_flag);
-      tc_fence_after();
-      qk(0, 0);
-      if (fc & kTwo) qk(1, 0);
-      mma_commit_if(lead, bar(K_FREE));
-      if (fc & kLast) mma_commit_if(lead, bar(Q_FREE));
-      for (uint32_t k = 0; fc & kMore; ++k) {
-        const bool more = fn & kMore, boundary = more && (fn & kStart);
-        wait_bar(bar(V_READY), k & 1u, p.err, abort_flag);
-        tc_fence_after();
-        pv(0, fc & kStart);
-        const uint32_t fnn = flags();                     // while the product runs
-        if (more && !boundary) {
-          wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
-          pv_done(0);
+      uint32_t sq[2] = {0, 0};                            // segments begun per tile
+      auto q_ready = [&](int t) {
+        wait(bar(Q_FP16 + t), sq[t] & 1u, abort_flag);
+        ++sq[t];
+      };
+      uint32_t fc = 0, fn = 0;                            // the current block's (k) and the next one's
+#pragma unroll 1
+      for (uint32_t k = ~0u - 1u;; ++k) {                 // (the first rounds have no current block, no next one)
+        const bool have = fc & kMore, more = fn & kMore, boundary = more && (fn & kStart);
+        if (have) {
+          wait(bar(V_READY), k & 1u, abort_flag);
           tc_fence_after();
-          qk(0, k + 1);
+          pv(0, fc & kStart);
         }
-        if (fc & kTwo) pv(1, fc & kStart);
-        mma_commit_if(lead, bar(V_FREE));
-        if (more) {
-          if (boundary) {
-            wait_bar(bar(Q_READY), sq & 1u, p.err, abort_flag);
-            ++sq;
-            wait_bar(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, p.err, abort_flag);
-            pv_done(0);
-            tc_fence_after();
-            qk(0, k + 1);
+        const uint32_t fnn = flags();                     // while the product runs
+        // Q K of the next block's first tile, then P V of this one's second; the
+        // other way round where the query rows change
+#pragma unroll 1
+        for (int step = 0; step < 2; ++step) {
+          if (step == boundary) {
+            if (more) {
+              if (boundary) q_ready(0);
+              wait(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, abort_flag);
+              pv_done(0);
+              tc_fence_after();
+              qk(0, k + 1);
+            }
+          } else if (have) {
+            if (fc & kTwo) pv(1, fc & kStart);
+            mma_commit_if(lead, bar(V_FREE));
           }
+        }
+        if (more) {
           if (fn & kTwo) {
+            if (boundary) q_ready(1);
             pv_done(1);
             tc_fence_after();
             qk(1, k + 1);
@@ -499,52 +616,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         fc = fn;
         fn = fnn;
+        if (!(fc | fn)) break;
       }
       __syncwarp();
     } else if (warp == 2) {
-      // ======================= Q loader =======================
-      if (lane == 0) {
-        uint32_t s = 0;
-        for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
-          if (!c.start) continue;
-          if (s > 0) wait_bar(bar(Q_FREE), (s - 1) & 1u, p.err, abort_flag);
-          if (*abort_flag) break;
-          ++s;
-          const int nt = walk.tiles(c), tok = c.s.q0 + c.it.r0 / G;
-          mbar_expect_tx(bar(Q_READY), static_cast<uint32_t>(nt * (D / 64) * TR * 128));
-          for (int t = 0; t < nt; ++t)
+      // ======================= Q loader, and the segments' powers =======================
+      // (a segment's are read before the last one's query rows are free: the decode
+      // warps are ahead of the MMAs)
+      uint32_t s = 0, loads[2] = {0, 0};                  // segments, and those of a tile
+#pragma unroll 1
+      for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
+        if (!c.start) continue;
+        const uint32_t x = __ldcg(p.tops + (static_cast<long long>(c.it.b) * H + c.h) * (2 * kParts) + lane);
+        const uint32_t ke = __reduce_max_sync(0xffffffffu, lane < kParts ? x : 0u);
+        const uint32_t ve = __reduce_max_sync(0xffffffffu, lane < kParts ? 0u : x);
+        if (lane == 0) {
+          s_pow[s & 3u] = make_int2(exponent(ke), exponent(ve));
+          mbar_arrive(bar(POWERS + (s & 3u)));
+        }
+        if (s > 0) wait(bar(Q_FREE), (s - 1) & 1u, abort_flag);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        ++s;
+        const int nt = walk.tiles(c), tok = c.s.q0 + c.it.r0 / G;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= nt) break;
+          ++loads[t];
+          if (lane == 0) {
+            mbar_expect_tx(bar(Q_READY + t), static_cast<uint32_t>((D / 64) * TR * 128));
+#pragma unroll 1
             for (int half = 0; half < D / 64; ++half)
               tma_load_4d(base + M::kQ + t * M::kTile + half * kTileHalf, &qmap, 64 * half, 0, c.h, tok + t * p.TT,
-                          bar(Q_READY));
+                          bar(Q_READY + t));
+          }
         }
-        if (*abort_flag && s > 0) drain(bar(Q_READY), (s - 1) & 1u);
       }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (*abort_flag && lane == 0 && loads[t] > 0) drain(bar(Q_READY + t), (loads[t] - 1) & 1u);
     } else if (warp >= 12) {
       // ======================= decode =======================
       const int wk = warp - 12;
-      Place kc = walk.begin(wr), vc = kc;
       const int half = wk >> 2;
-      uint32_t slot = half, wraps = 0, kb = 0, vb = 0, seg = 0;
-      auto decode = [&](const Place& c, bool is_v) {
-        const uint32_t x = is_v ? vb : kb;
-        wait_bar(bar(RING_FULL + 2 * slot + half), wraps >> (nu & 1u) & 1u, p.err, abort_flag);
-        const uint32_t buf = is_v ? 0 : x & 1u;
-        if (is_v && x >= 1) wait_bar(bar(V_FREE), (x - 1) & 1u, p.err, abort_flag);
-        if (!is_v && x >= 2) wait_bar(bar(K_FREE + buf), ((x >> 1) - 1) & 1u, p.err, abort_flag);
-        const unsigned char* u = sm + M::kRing + slot * unit_bytes;
-        const int t0 = c.j * kBT, nv = min(kBT, c.s.len - t0);
-        unsigned char* dst = sm + (is_v ? M::kV : M::kK) + buf * M::kTile;
-        if (is_v) {
-          if (c.start) ++seg;
-          decode_unit<BITS, D, true>(u, dst, wk, lane, nv, t0, static_cast<unsigned long long>(seg) << 32,
-                                     s_bad + (seg & 7u));
-        } else {
-          decode_unit<BITS, D, false>(u, dst, wk, lane, nv, 0, 0, nullptr);
-        }
+      uint32_t slot = half, wraps = 0, kb = 0, seg = 0;    // kb: K blocks decoded; V's are one behind
+      Place c = walk.begin(wr);
+      int t0 = 0, nv = 0;                                 // V's block
+      bool start = false;
+      uint32_t segs = 0;                                  // segments begun
+      int2 pw = make_int2(0, 0);                          // K's and V's block's
+      int ev = 0;
+      auto arrived = [&]() {
+        wait(bar(RING_FULL + 2 * slot + half), wraps >> (nu & 1u) & 1u, abort_flag);
+        return sm + M::kRing + slot * unit_bytes;
+      };
+      auto finished = [&](uint32_t ready) {
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar((is_v ? V_READY : K_READY) + buf));
+          mbar_arrive(ready);
           mbar_arrive(bar(RING_EMPTY + slot));
         }
         slot += 2;
@@ -552,17 +681,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           slot -= nu;
           ++wraps;
         }
-        if (is_v) ++vb; else ++kb;
       };
-      decode(kc, false);
-      walk.next(kc);
-      while (vc.left > 0) {
-        if (kc.left > 0) {
-          decode(kc, false);
-          walk.next(kc);
+#pragma unroll 1
+      for (;; ++kb) {                                     // K(kb), then V(kb - 1)
+        const int t0_k = c.j * kBT, nv_k = c.s.len - t0_k;
+        const bool more = c.left > 0, start_k = c.start;
+        if (more) {
+          const uint32_t buf = kb & 1u;
+          if (start_k) {
+            wait(bar(POWERS + (segs & 3u)), segs >> 2 & 1u, abort_flag);
+            pw = s_pow[segs & 3u];
+            ++segs;
+          }
+          const unsigned char* u = arrived();
+          if (kb >= 2) wait(bar(K_FREE + buf), ((kb >> 1) - 1) & 1u, abort_flag);
+          decode_unit<BITS, D, false>(u, sm + M::kK + buf * M::kTile, wk, lane, min(kBT, nv_k),
+                                      exp2i(kTop - pw.x), 0, 0, nullptr);
+          finished(bar(K_READY + buf));
+          walk.next(c);
         }
-        decode(vc, true);
-        walk.next(vc);
+        if (kb > 0) {
+          const uint32_t v = kb - 1;
+          const unsigned char* u = arrived();
+          if (v >= 1) wait(bar(V_FREE), (v - 1) & 1u, abort_flag);
+          if (start) ++seg;
+          decode_unit<BITS, D, true>(u, sm + M::kV, wk, lane, min(kBT, nv), exp2i(kTop - ev), t0,
+                                     static_cast<unsigned long long>(seg) << 32, s_bad + (seg & 7u));
+          finished(bar(V_READY));
+        }
+        if (!more) break;
+        t0 = t0_k;
+        nv = nv_k;
+        start = start_k;
+        ev = pw.y;
       }
     } else if (warp >= 4) {
       // ======================= softmax: one query row per thread =======================
@@ -573,12 +724,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       const uint32_t o_col = tmem + lane_addr + 256u + 128u * tile;
       const bool neg = p.qscale < 0.f;
       float m_ref = -INFINITY, z = 0.f;
-      uint32_t k = 0, seg = 0;                            // blocks of this tile, segments of the CTA
+      float qs = 0.f, q_next = 0.f;                       // the row's factor of the scores; the next segment's
+      float ov = 0.f, ov_next = 0.f;                      // what O is multiplied by
+      uint32_t k = 0, seg = 0, nq = 0;                    // blocks of this tile, segments of the CTA, of this tile
       int lim = 0;                                        // keys the row sees
       bool real = false;                                  // the row exists
       bool first_seg = true, seg_is_first = true, from_zero = false;
-      for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
-        if (c.start) {
+      Place c = walk.begin(wr);
+#pragma unroll 1
+      for (bool block = false;; block = true) {           // (the first round only turns the first query rows)
+        bool end = false, whole = false, poison = false;
+        long long row = 0;
+        if (block && c.start) {
           ++seg;
           seg_is_first = first_seg;
           first_seg = false;
@@ -588,116 +745,137 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           lim = real ? row_limit(p.t, c.s, rr) : c.s.len;  // rows that do not exist take the unmasked path
           m_ref = -INFINITY;
           z = 0.f;
+          qs = q_next;
+          ov = ov_next;
         }
-        if (walk.tiles(c) <= tile) continue;
-        wait_bar(bar(S_FULL + tile), k & 1u, p.err, abort_flag);
-        tc_fence_after();
-        const int nv = min(kBT, lim - c.j * kBT);         // columns the row sees
-        const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
-        // the row's extreme over the columns it sees
-        float mb;
-        if (plain) {
-          float mx = -INFINITY;
+        if (block && walk.tiles(c) > tile) {
+          wait(bar(S_FULL + tile), k & 1u, abort_flag);
+          tc_fence_after();
+          const int nv = min(kBT, lim - c.j * kBT);       // columns the row sees
+          const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
+          const int seen = plain ? kBT : __reduce_max_sync(0xffffffffu, nv);   // columns that a row of the warp sees
+          // the row's largest score over the columns it sees (none: never a new reference)
+          float mb = -INFINITY;
+          if (plain) {
 #pragma unroll 1
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t sr[64];
-            KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
-            KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
-            tmem_wait_ld();
-            mx = fmaxf(mx, row_max(sr));
-          }
-          mb = mx * p.qscale;
-        } else {
-          float mx = neg ? INFINITY : -INFINITY;
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            uint32_t sr[16];
-            KVQ_LD16(sr, s_col + 16u * cc);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = __uint_as_float(sr[e]);
-              if (16 * cc + e < nv) mx = neg ? fminf(mx, x) : fmaxf(mx, x);
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t sr[64];
+              KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
+              KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+              tmem_wait_ld();
+              mb = fmaxf(mb, row_max(sr));
             }
-          }
-          mb = nv > 0 ? mx * p.qscale : -INFINITY;        // (none seen: never a new reference)
-        }
-        const bool need = mb > m_ref + kLazy;
-        if (__any_sync(0xffffffffu, need)) {
-          const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
-          if (need) m_ref = mb;
-          z *= a;
-          if (!c.start) {
+            mb *= qs;
+          } else {
 #pragma unroll 1
-            for (int oc = 0; oc < D / 16; ++oc) {
-              uint32_t orr[16];
-              KVQ_LD16(orr, o_col + 16u * oc);
+            for (int cc = 0; 16 * cc < seen; ++cc) {
+              uint32_t sr[16];
+              KVQ_LD16(sr, s_col + 16u * cc);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
-              KVQ_ST16(o_col + 16u * oc, orr);
+              for (int e = 0; e < 16; ++e)
+                if (16 * cc + e < nv) mb = fmaxf(mb, __uint_as_float(sr[e]) * qs);
             }
+          }
+          const bool need = mb > m_ref + kLazy;
+          if (__any_sync(0xffffffffu, need)) {
+            const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
+            if (need) m_ref = mb;
+            z *= a;
+            if (!c.start) {
+#pragma unroll 1
+              for (int oc = 0; oc < D / 16; ++oc) {
+                uint32_t orr[16];
+                KVQ_LD16(orr, o_col + 16u * oc);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+                KVQ_ST16(o_col + 16u * oc, orr);
+              }
+            }
+          }
+          // p = exp2(s * qs - m_ref + kTopP) as fp16 over the columns already read,
+          // 16 at a time, the next ones on their way
+          const float m_top = kTopP - m_ref;
+          u64 z2 = 0ull;
+          if (plain) {
+            uint32_t s0[16], s1[16];
+            const u64 f2 = pack2(qs, qs), c2 = pack2(m_top, m_top);
+            auto columns = [&](const uint32_t (&sr)[16], int cc) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, c2);
+                const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
+                z2 = add2(z2, pack2(p0, p1));
+                pk[e] = pack_f16(p0, p1);
+              }
+              KVQ_ST8(s_col + 8u * cc, pk);
+            };
+            KVQ_LD16(s0, s_col);
+#pragma unroll 1
+            for (int cc = 0; cc < 8; cc += 2) {
+              tmem_wait_ld();
+              KVQ_LD16(s1, s_col + 16u * cc + 16u);
+              columns(s0, cc);
+              tmem_wait_ld();
+              if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
+              columns(s1, cc + 1);
+            }
+          } else {
+#pragma unroll 1
+            for (int cc = 0; cc < 8; ++cc) {
+              const int left = nv - 16 * cc;
+              uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+              if (16 * cc < seen) {
+                uint32_t sr[16];
+                KVQ_LD16(sr, s_col + 16u * cc);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const float p0 = e < left ? ex2(fmaf(__uint_as_float(sr[e]), qs, m_top)) : 0.f;
+                  const float p1 = e + 1 < left ? ex2(fmaf(__uint_as_float(sr[e + 1]), qs, m_top)) : 0.f;
+                  z2 = add2(z2, pack2(p0, p1));
+                  pk[e >> 1] = pack_f16(p0, p1);
+                }
+              }
+              KVQ_ST8(s_col + 8u * cc, pk);
+            }
+          }
+          z += lo_f(z2) + hi_f(z2);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(P_FULL + tile));
+          ++k;
+          end = walk.last(c);
+          if (end) {
+            whole = from_zero && c.j + 1 == c.nb;
+            const int rr = c.it.r0 + tile * TR + r;
+            row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
           }
         }
-        // p = exp2(s * qscale - m_ref) as bf16 over the columns already read,
-        // 16 at a time, the next ones on their way
-        const u64 qs2 = pack2(p.qscale, p.qscale), nm2 = pack2(-m_ref, -m_ref);
-        u64 z2 = 0ull;
-        if (plain) {
-          uint32_t s0[16], s1[16];
-          auto columns = [&](const uint32_t (&sr)[16], int cc) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
-              const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
-              z2 = add2(z2, pack2(p0, p1));
-              pk[e] = pack_bf16(p0, p1);
-            }
-            KVQ_ST8(s_col + 8u * cc, pk);
-          };
-          KVQ_LD16(s0, s_col);
-#pragma unroll 1
-          for (int cc = 0; cc < 8; cc += 2) {
-            tmem_wait_ld();
-            KVQ_LD16(s1, s_col + 16u * cc + 16u);
-            columns(s0, cc);
-            tmem_wait_ld();
-            if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
-            columns(s1, cc + 1);
-          }
-        } else {
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            const int left = nv - 16 * cc;
-            uint32_t sr[16], pk[8];
-            KVQ_LD16(sr, s_col + 16u * cc);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), qs2, nm2);
-              const float p0 = 2 * e < left ? ex2(lo_f(x)) : 0.f;
-              const float p1 = 2 * e + 1 < left ? ex2(hi_f(x)) : 0.f;
-              z2 = add2(z2, pack2(p0, p1));
-              pk[e] = pack_bf16(p0, p1);
-            }
-            KVQ_ST8(s_col + 8u * cc, pk);
-          }
+        if (block) {
+          walk.next(c);
         }
-        z += lo_f(z2) + hi_f(z2);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P_FULL + tile));
-        if (walk.last(c)) {
+        // the next segment's query rows; before this one's own end, so that its
+        // first scores are computed meanwhile
+        if (c.left > 0 && c.start && walk.tiles(c) > tile) {
+          wait(bar(Q_READY + tile), nq & 1u, abort_flag);
+          ++nq;
+          const int2 pw = s_pow[seg & 3u];                 // (written before the rows were asked for)
+          q_next = p.qscale * exp2i(pw.x - kTop) * (r < TR ? row_to_f16<D>(sm + M::kQ + tile * M::kTile, r) : 1.f);
+          ov_next = exp2i(pw.y - kTop);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Q_FP16 + tile));
+        }
+        if (end) {
           // the segment's last P V product must be done before O is read
-          wait_bar(bar(PV_DONE + tile), k & 1u, p.err, abort_flag);
+          wait(bar(PV_DONE + tile), (k - 1) & 1u, abort_flag);
           tc_fence_after();
-          const bool whole = from_zero && c.j + 1 == c.nb;
           const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
-          const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
-          const int rr = c.it.r0 + tile * TR + r;
-          const long long row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
+          poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
           const int pr = tile * 128 + r;
           float* part = p.partials + (2 * static_cast<long long>(blockIdx.x) + (seg_is_first ? 0 : 1)) * 256 * (D + 2) +
                         static_cast<long long>(pr >> 5) * (D + 2) * 32 + (pr & 31);
@@ -706,8 +884,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             part[32] = z;
           }
           // z = 0: a row without a key
-          const float inv = poison ? __uint_as_float(0x7fc00000u) : (z == 0.f ? 0.f : 1.f / z);
-          const float keep = poison ? inv : 1.f;
+          const float inv = poison ? __uint_as_float(0x7fc00000u) : (z == 0.f ? 0.f : ov / z);
+          const float keep = poison ? inv : ov;
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t orr[32];
@@ -731,12 +909,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
           tc_fence_before();
         }
-        ++k;
+        if (c.left <= 0) break;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) record_error(p.err, KVQ_ERR_TIMEOUT);
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -764,8 +943,11 @@ bool applies(const AttendArgs& a) {
   return a.g.group == 32 && (a.g.D == 64 || a.g.D == 128) && a.q_dtype == KVQ_BF16 && a.G <= 128 &&
          static_cast<long long>(a.max_q) * a.G > 16 && smem_of(a) <= 227 * 1024;
 }
+size_t partials_bytes(const AttendArgs& a) {
+  return 2 * static_cast<size_t>(ctas(a)) * 256 * (a.g.D + 2) * sizeof(float);
+}
 size_t workspace(const AttendArgs& a) {
-  return plan_bytes(a, item_rows(a)) + 2 * static_cast<size_t>(ctas(a)) * 256 * (a.g.D + 2) * sizeof(float);
+  return plan_bytes(a, item_rows(a)) + partials_bytes(a) + 2 * sizeof(uint32_t) * kParts * a.S * a.g.H_kv;
 }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link)
@@ -816,6 +998,8 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
   p.qscale = a.scale * kLog2e;
   p.O = static_cast<__nv_bfloat16*>(a.O);
   p.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan_bytes(a, RI));
+  uint32_t* tops = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(p.partials) + partials_bytes(a));
+  p.tops = tops;
   p.ctas = ctas(a);
   p.RI = RI;
   p.TT = tile_tokens(a);
@@ -825,6 +1009,10 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
     const kvq_status st = launch_plan(a, p.plan, RI, kBT, s);
     if (st != KVQ_OK) return st;
   }
+  if (launch_pdl(a.g.D == 64 ? paged_scales_kernel<64> : paged_scales_kernel<128>, dim3(a.S, a.g.H_kv, kParts),
+                 dim3(32 * kScanWarps), 0, s, p.t, p.k_scales, p.v_scales, tops, p.err) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  count_launch();
   const size_t smem = smem_of(a);
   auto kernel = a.g.D == 64 ? (a.g.bits == 4 ? paged_chunk_kernel<4, 64> : paged_chunk_kernel<8, 64>)
                             : (a.g.bits == 4 ? paged_chunk_kernel<4, 128> : paged_chunk_kernel<8, 128>);

@@ -201,6 +201,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // UMMA shared-memory descriptor: 128-byte swizzle, 1 KB eight-row atoms.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) |
@@ -211,6 +217,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo_bytes,
 __host__ __device__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? (1u << 16) : 0u) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// The same with fp16 A and B.
+__host__ __device__ constexpr uint32_t instr_desc_f16(int n, bool b_mn_major) {
+  return instr_desc(n, b_mn_major) & ~((7u << 7) | (7u << 10));
 }
 
 // Byte offset of 16-byte chunk `c` (0..7) of row `r` inside a swizzled 64-wide half.
