@@ -43,6 +43,9 @@
 // Shared-memory tiles use the 128-byte-swizzled UMMA layout of tc_common.cuh.
 #include <cuda.h>
 
+#include <algorithm>
+#include <type_traits>
+
 #include "f32x2.cuh"
 #include "paged.cuh"
 #include "tc_common.cuh"
@@ -71,7 +74,7 @@ constexpr int kMaxUnits = 12;                    // half-units of the ring
 constexpr int kTop = 7, kTopQ = 14;
 constexpr float kTopP = 7.f;                     // p <= 2^(kTopP + kLazy) = 2^15
 constexpr int kExpMin = -100, kExpMax = 127;
-constexpr int kParts = 16;                       // of a sequence's groups, each with a maximum of its own
+constexpr int kParts = 16;                       // of a sequence's groups, at most, each with a maximum of its own
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 // exponent of a value given by its bits
@@ -88,7 +91,7 @@ struct Smem {
   static constexpr int kRing = kV + kTile;
   static constexpr int kRingBytes = 55 * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 58 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kMisc = kBar + 54 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
   static constexpr int kPow = kMisc + 80;          // int2 [4]: a segment's exponents (K, V)
   static constexpr int kPre = kPow + 32;            // int pre[S + 1] (inline plan)
 };
@@ -103,10 +106,9 @@ enum Bar {
   S_FULL = 42,                   // [2]
   P_FULL = 44,                   // [2]
   PV_DONE = 46,                  // [2]
-  Q_READY = 48,                  // [2]
-  Q_FP16 = 50,                   // [2]
-  Q_FREE = 52,
-  POWERS = 53,                   // [4]
+  Q_READY = 48,
+  Q_FREE = 49,
+  POWERS = 50,                   // [4]
 };
 
 struct Params {
@@ -117,6 +119,8 @@ struct Params {
   const uint8_t* v_codes;
   const float* v_scales;
   const uint32_t* tops;          // [S][H][2][kParts]: bits of the largest K and V scales
+  int parts;                     // of them in use
+  const float* q_pow;            // [T][H_q]: 2^(e - kTopQ) of a query row
   float qscale;                  // scale * log2(e)
   __nv_bfloat16* O;
   float* partials;               // [2 ctas][8][D + 2][32]
@@ -280,32 +284,6 @@ __device__ __forceinline__ float row_max(const uint32_t (&sr)[64]) {
   return max3(max3(acc[0], acc[1], acc[2]), max3(acc[3], acc[4], acc[5]), fmaxf(acc[6], acc[7]));
 }
 
-// A query row of a tile from bf16 to fp16, in place, with the power of two that
-// takes its largest element into [2^kTopQ, 2^(kTopQ + 1)); returns the inverse.
-template <int D>
-__device__ __forceinline__ float row_to_f16(unsigned char* tile, int r) {
-  auto chunk = [&](int ch) { return reinterpret_cast<uint4*>(tile + (ch >> 3) * kTileHalf + swz(r, ch & 7)); };
-  uint32_t m = 0;                                  // (magnitudes order as their bits do)
-#pragma unroll 2
-  for (int ch = 0; ch < D / 8; ++ch) {
-    const uint4 x = *chunk(ch);
-    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-  }
-  m = max(m & 0xffffu, m >> 16);
-  const int e = min(max(static_cast<int>(m >> 7) - 127, kExpMin), kExpMax);
-  const float f = exp2i(kTopQ - e);
-  auto turn = [&](uint32_t v) {
-    return pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
-  };
-#pragma unroll 2
-  for (int ch = 0; ch < D / 8; ++ch) {
-    const uint4 x = *chunk(ch);
-    *chunk(ch) = make_uint4(turn(x.x), turn(x.y), turn(x.z), turn(x.w));
-  }
-  return exp2i(e - kTopQ);
-}
-
 // Bounded wait: after about two seconds raises the CTA's abort flag and goes on;
 // once the flag is up every later wait gives up too, and the CTA records
 // KVQ_ERR_TIMEOUT as it ends.
@@ -327,40 +305,88 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   }
 }
 
-// The largest K and V scales of a sequence and KV head, in kParts parts of its
-// groups of 32 tokens: a warp a group, a CTA a part.  It reads the scales alone
-// (32 of 160 bytes a token at D = 128 and 4 bits), and the attention finds them
-// in the L2 afterwards.
-constexpr int kScanWarps = 8;
+// What the attention needs beforehand.  The first S * H * parts CTAs find the
+// largest K and V scales of a sequence and KV head, in parts of its groups of 32
+// tokens, a warp a group: they read the scales alone (32 of 160 bytes a token at D
+// = 128 and 4 bits), and the attention finds them in the L2 afterwards.  The
+// others turn the query rows to fp16, D / 8 lanes a row.  (Turned in shared memory
+// by the softmax, at a segment's start, prompts took 419 us instead of 397.)
+constexpr int kPrepareWarps = 8, kRowsPerLane = 4;
 template <int D>
-__global__ void __launch_bounds__(32 * kScanWarps) paged_scales_kernel(Batch t, const float* k_scales,
-                                                                       const float* v_scales, uint32_t* tops,
-                                                                       unsigned int* err) {
+__global__ void __launch_bounds__(32 * kPrepareWarps)
+    paged_prepare_kernel(Batch t, const float* k_scales, const float* v_scales, uint32_t* tops, int parts,
+                         const uint4* Q, uint4* Qh, float* q_pow, long long rows, unsigned int* err) {
   griddep_wait();
-  const int b = blockIdx.x, h = blockIdx.y, part = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long scans = static_cast<long long>(t.S) * t.H * parts;
+  if (blockIdx.x >= scans) {
+    constexpr int L = D / 8, PASS = 32 * kPrepareWarps / L;
+    const long long first = (blockIdx.x - scans) * (PASS * kRowsPerLane) + threadIdx.x / L;
+    const int l = threadIdx.x % L;
+    uint4 x[kRowsPerLane];
+#pragma unroll
+    for (int i = 0; i < kRowsPerLane; ++i) {
+      const long long row = first + i * PASS;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows) x[i] = __ldg(Q + row * L + l);
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsPerLane; ++i) {
+      const long long row = first + i * PASS;
+      uint32_t m = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                            __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));   // (magnitudes order as their bits do)
+      m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int e = exponent(m << 16);
+      const float f = exp2i(kTopQ - e);
+      auto turn = [&](uint32_t v) {
+        return pack_f16(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xffff0000u) * f);
+      };
+      if (row < rows) {
+        Qh[row * L + l] = make_uint4(turn(x[i].x), turn(x[i].y), turn(x[i].z), turn(x[i].w));
+        if (l == 0) q_pow[row] = exp2i(e - kTopQ);
+      }
+    }
+    return;
+  }
+  const int part = static_cast<int>(blockIdx.x % parts), bh = static_cast<int>(blockIdx.x / parts);
+  const int b = bh / t.H, h = bh % t.H;
   const SeqView s = seq_view(t, b);
   const int32_t* table = t.table + static_cast<long long>(b) * t.max_pages;
   uint32_t top[2] = {0u, 0u};
-  if (s.n > 0)
-#pragma unroll 4
-    for (int g = part * kScanWarps + warp; 32 * g < s.len; g += kParts * kScanWarps) {
+  // lane i looks up the page of the warp's i-th group, 32 at a time; then the
+  // scales of four groups are on their way together
+  const int stride = parts * kPrepareWarps, groups = s.n > 0 ? (s.len + 31) >> 5 : 0;
+  for (int g0 = part * kPrepareWarps + warp; g0 < groups; g0 += 32 * stride) {
+    const int g = g0 + lane * stride;
+    long long own = 0;
+    if (g < groups) {
       const int pi = 32 * g / t.P;
-      const long long tok =
-          (static_cast<long long>(read_page(__ldg(table + pi), t.pages, err)) * t.H + h) * t.P + 32 * g - pi * t.P;
-      const float* at[2] = {k_scales + (tok >> 5) * D + lane * (D / 32), v_scales + (tok + lane) * (D / 32)};
+      own = (static_cast<long long>(read_page(__ldg(table + pi), t.pages, err)) * t.H + h) * t.P + 32 * g - pi * t.P;
+    }
+    const int n = min(32, (groups - g0 + stride - 1) / stride);
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      using Vec = typename std::conditional<D == 128, uint4, uint2>::type;
+      Vec x[4][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        __align__(16) float x[D / 32];
-        if (D == 128) *reinterpret_cast<float4*>(x) = __ldg(reinterpret_cast<const float4*>(at[i]));
-        else *reinterpret_cast<float2*>(x) = __ldg(reinterpret_cast<const float2*>(at[i]));
+      for (int i = 0; i < 4; ++i) {                       // (past the last one: the last one again)
+        const long long tok = __shfl_sync(0xffffffffu, own, min(i0 + i, n - 1));
+        x[i][0] = __ldg(reinterpret_cast<const Vec*>(k_scales + (tok >> 5) * D) + lane);
+        x[i][1] = __ldg(reinterpret_cast<const Vec*>(v_scales + tok * (D / 32)) + lane);
+      }
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {                // (what is not finite stays that whatever the power)
-          const uint32_t v = __float_as_uint(x[e]) & 0x7fffffffu;
-          if (v < 0x7f800000u && (i == 0 || 32 * g + lane < s.len)) top[i] = max(top[i], v);
+      for (int i = 0; i < 4; ++i) {
+        const bool live = 32 * (g0 + min(i0 + i, n - 1) * stride) + lane < s.len;   // the lane's token
+#pragma unroll
+        for (int e = 0; e < 2 * D / 32; ++e) {            // (what is not finite stays that whatever the power)
+          const uint32_t v = reinterpret_cast<const uint32_t*>(&x[i][e / (D / 32)])[e % (D / 32)] & 0x7fffffffu;
+          if (v < 0x7f800000u && (e < D / 32 || live)) top[e / (D / 32)] = max(top[e / (D / 32)], v);
         }
       }
     }
-  __shared__ uint32_t s_top[2][kScanWarps];
+  }
+  __shared__ uint32_t s_top[2][kPrepareWarps];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, top[i]);
@@ -369,8 +395,8 @@ __global__ void __launch_bounds__(32 * kScanWarps) paged_scales_kernel(Batch t, 
   __syncthreads();
   if (threadIdx.x < 2) {
     uint32_t m = 0u;
-    for (int w = 0; w < kScanWarps; ++w) m = max(m, s_top[threadIdx.x][w]);
-    tops[((static_cast<long long>(b) * t.H + h) * 2 + threadIdx.x) * kParts + part] = m;
+    for (int w = 0; w < kPrepareWarps; ++w) m = max(m, s_top[threadIdx.x][w]);
+    tops[(static_cast<long long>(bh) * 2 + threadIdx.x) * kParts + part] = m;
   }
 }
 
@@ -411,12 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init(bar(S_FULL + i), 1);
       mbar_init(bar(P_FULL + i), 4);
       mbar_init(bar(PV_DONE + i), 1);
-      mbar_init(bar(Q_READY + i), 1);
-      mbar_init(bar(Q_FP16 + i), 4);
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(POWERS + i), 1);
     mbar_init(bar(V_READY), kDecodeWarps);
     mbar_init(bar(V_FREE), 1);
+    mbar_init(bar(Q_READY), 1);
     mbar_init(bar(Q_FREE), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -572,11 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         walk.next(c);
         return __shfl_sync(0xffffffffu, f, 0);
       };
-      uint32_t sq[2] = {0, 0};                            // segments begun per tile
-      auto q_ready = [&](int t) {
-        wait(bar(Q_FP16 + t), sq[t] & 1u, abort_flag);
-        ++sq[t];
-      };
+      uint32_t sq = 0;                                    // segments begun
       uint32_t fc = 0, fn = 0;                            // the current block's (k) and the next one's
 #pragma unroll 1
       for (uint32_t k = ~0u - 1u;; ++k) {                 // (the first rounds have no current block, no next one)
@@ -593,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         for (int step = 0; step < 2; ++step) {
           if (step == boundary) {
             if (more) {
-              if (boundary) q_ready(0);
+              if (boundary) wait(bar(Q_READY), sq++ & 1u, abort_flag);
               wait(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, abort_flag);
               pv_done(0);
               tc_fence_after();
@@ -606,7 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         if (more) {
           if (fn & kTwo) {
-            if (boundary) q_ready(1);
             pv_done(1);
             tc_fence_after();
             qk(1, k + 1);
@@ -623,13 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // ======================= Q loader, and the segments' powers =======================
       // (a segment's are read before the last one's query rows are free: the decode
       // warps are ahead of the MMAs)
-      uint32_t s = 0, loads[2] = {0, 0};                  // segments, and those of a tile
+      uint32_t s = 0;                                     // segments
 #pragma unroll 1
       for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
         if (!c.start) continue;
         const uint32_t x = __ldcg(p.tops + (static_cast<long long>(c.it.b) * H + c.h) * (2 * kParts) + lane);
-        const uint32_t ke = __reduce_max_sync(0xffffffffu, lane < kParts ? x : 0u);
-        const uint32_t ve = __reduce_max_sync(0xffffffffu, lane < kParts ? 0u : x);
+        const uint32_t ke = __reduce_max_sync(0xffffffffu, lane < p.parts ? x : 0u);
+        const uint32_t ve = __reduce_max_sync(0xffffffffu, lane >= kParts && lane < kParts + p.parts ? x : 0u);
         if (lane == 0) {
           s_pow[s & 3u] = make_int2(exponent(ke), exponent(ve));
           mbar_arrive(bar(POWERS + (s & 3u)));
@@ -638,22 +658,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         if (__any_sync(0xffffffffu, *abort_flag)) break;
         ++s;
         const int nt = walk.tiles(c), tok = c.s.q0 + c.it.r0 / G;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t >= nt) break;
-          ++loads[t];
-          if (lane == 0) {
-            mbar_expect_tx(bar(Q_READY + t), static_cast<uint32_t>((D / 64) * TR * 128));
+        if (lane == 0) {
+          mbar_expect_tx(bar(Q_READY), static_cast<uint32_t>(nt * (D / 64) * TR * 128));
 #pragma unroll 1
-            for (int half = 0; half < D / 64; ++half)
-              tma_load_4d(base + M::kQ + t * M::kTile + half * kTileHalf, &qmap, 64 * half, 0, c.h, tok + t * p.TT,
-                          bar(Q_READY + t));
+          for (int i = 0; i < nt * (D / 64); ++i) {
+            const int t = i / (D / 64), half = i % (D / 64);
+            tma_load_4d(base + M::kQ + t * M::kTile + half * kTileHalf, &qmap, 64 * half, 0, c.h, tok + t * p.TT,
+                        bar(Q_READY));
           }
         }
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (*abort_flag && lane == 0 && loads[t] > 0) drain(bar(Q_READY + t), (loads[t] - 1) & 1u);
+      if (*abort_flag && lane == 0 && s > 0) drain(bar(Q_READY), (s - 1) & 1u);
     } else if (warp >= 12) {
       // ======================= decode =======================
       const int wk = warp - 12;
@@ -724,18 +739,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       const uint32_t o_col = tmem + lane_addr + 256u + 128u * tile;
       const bool neg = p.qscale < 0.f;
       float m_ref = -INFINITY, z = 0.f;
-      float qs = 0.f, q_next = 0.f;                       // the row's factor of the scores; the next segment's
-      float ov = 0.f, ov_next = 0.f;                      // what O is multiplied by
-      uint32_t k = 0, seg = 0, nq = 0;                    // blocks of this tile, segments of the CTA, of this tile
+      float qs = 0.f, ov = 0.f;                           // what the row's scores and its O are multiplied by
+      uint32_t k = 0, seg = 0;                            // blocks of this tile, segments of the CTA
+      long long row = 0;                                  // of Q and O
       int lim = 0;                                        // keys the row sees
       bool real = false;                                  // the row exists
       bool first_seg = true, seg_is_first = true, from_zero = false;
-      Place c = walk.begin(wr);
 #pragma unroll 1
-      for (bool block = false;; block = true) {           // (the first round only turns the first query rows)
-        bool end = false, whole = false, poison = false;
-        long long row = 0;
-        if (block && c.start) {
+      for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
+        if (c.start) {
           ++seg;
           seg_is_first = first_seg;
           first_seg = false;
@@ -743,139 +755,123 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           const int rr = c.it.r0 + tile * TR + r;
           real = r < TR && rr < c.s.n * G;
           lim = real ? row_limit(p.t, c.s, rr) : c.s.len;  // rows that do not exist take the unmasked path
+          row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
           m_ref = -INFINITY;
           z = 0.f;
-          qs = q_next;
-          ov = ov_next;
+          qs = real ? p.qscale * __ldcg(p.q_pow + row) : 0.f;   // (no row: equal scores, never a new reference)
         }
-        if (block && walk.tiles(c) > tile) {
-          wait(bar(S_FULL + tile), k & 1u, abort_flag);
-          tc_fence_after();
-          const int nv = min(kBT, lim - c.j * kBT);       // columns the row sees
-          const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
-          const int seen = plain ? kBT : __reduce_max_sync(0xffffffffu, nv);   // columns that a row of the warp sees
-          // the row's largest score over the columns it sees (none: never a new reference)
-          float mb = -INFINITY;
-          if (plain) {
+        if (walk.tiles(c) <= tile) continue;
+        wait(bar(S_FULL + tile), k & 1u, abort_flag);
+        if (c.start) {                                    // (written before the query rows were asked for)
+          const int2 pw = s_pow[(seg - 1) & 3u];
+          qs *= exp2i(pw.x - kTop);
+          ov = exp2i(pw.y - kTop);
+        }
+        tc_fence_after();
+        const int nv = min(kBT, lim - c.j * kBT);       // columns the row sees
+        const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
+        const int seen = plain ? kBT : __reduce_max_sync(0xffffffffu, nv);   // columns that a row of the warp sees
+        // the row's largest score over the columns it sees (none: never a new reference)
+        float mb = -INFINITY;
+        if (plain) {
 #pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t sr[64];
-              KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
-              KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t sr[64];
+            KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
+            KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+            tmem_wait_ld();
+            mb = fmaxf(mb, row_max(sr));
+          }
+          mb *= qs;
+        } else {
+#pragma unroll 1
+          for (int cc = 0; 16 * cc < seen; ++cc) {
+            uint32_t sr[16];
+            KVQ_LD16(sr, s_col + 16u * cc);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (16 * cc + e < nv) mb = fmaxf(mb, __uint_as_float(sr[e]) * qs);
+          }
+        }
+        const bool need = mb > m_ref + kLazy;
+        if (__any_sync(0xffffffffu, need)) {
+          const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
+          if (need) m_ref = mb;
+          z *= a;
+          if (!c.start) {
+#pragma unroll 1
+            for (int oc = 0; oc < D / 16; ++oc) {
+              uint32_t orr[16];
+              KVQ_LD16(orr, o_col + 16u * oc);
               tmem_wait_ld();
-              mb = fmaxf(mb, row_max(sr));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+              KVQ_ST16(o_col + 16u * oc, orr);
             }
-            mb *= qs;
-          } else {
+          }
+        }
+        // p = exp2(s * qs - m_ref + kTopP) as fp16 over the columns already read,
+        // 16 at a time, the next ones on their way
+        const float m_top = kTopP - m_ref;
+        u64 z2 = 0ull;
+        if (plain) {
+          uint32_t s0[16], s1[16];
+          const u64 f2 = pack2(qs, qs), c2 = pack2(m_top, m_top);
+          auto columns = [&](const uint32_t (&sr)[16], int cc) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, c2);
+              const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
+              z2 = add2(z2, pack2(p0, p1));
+              pk[e] = pack_f16(p0, p1);
+            }
+            KVQ_ST8(s_col + 8u * cc, pk);
+          };
+          KVQ_LD16(s0, s_col);
 #pragma unroll 1
-            for (int cc = 0; 16 * cc < seen; ++cc) {
+          for (int cc = 0; cc < 8; cc += 2) {
+            tmem_wait_ld();
+            KVQ_LD16(s1, s_col + 16u * cc + 16u);
+            columns(s0, cc);
+            tmem_wait_ld();
+            if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
+            columns(s1, cc + 1);
+          }
+        } else {
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            const int left = nv - 16 * cc;
+            uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            if (16 * cc < seen) {
               uint32_t sr[16];
               KVQ_LD16(sr, s_col + 16u * cc);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (16 * cc + e < nv) mb = fmaxf(mb, __uint_as_float(sr[e]) * qs);
-            }
-          }
-          const bool need = mb > m_ref + kLazy;
-          if (__any_sync(0xffffffffu, need)) {
-            const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
-            if (need) m_ref = mb;
-            z *= a;
-            if (!c.start) {
-#pragma unroll 1
-              for (int oc = 0; oc < D / 16; ++oc) {
-                uint32_t orr[16];
-                KVQ_LD16(orr, o_col + 16u * oc);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
-                KVQ_ST16(o_col + 16u * oc, orr);
-              }
-            }
-          }
-          // p = exp2(s * qs - m_ref + kTopP) as fp16 over the columns already read,
-          // 16 at a time, the next ones on their way
-          const float m_top = kTopP - m_ref;
-          u64 z2 = 0ull;
-          if (plain) {
-            uint32_t s0[16], s1[16];
-            const u64 f2 = pack2(qs, qs), c2 = pack2(m_top, m_top);
-            auto columns = [&](const uint32_t (&sr)[16], int cc) {
-              uint32_t pk[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, c2);
-                const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
+              for (int e = 0; e < 16; e += 2) {
+                const float p0 = e < left ? ex2(fmaf(__uint_as_float(sr[e]), qs, m_top)) : 0.f;
+                const float p1 = e + 1 < left ? ex2(fmaf(__uint_as_float(sr[e + 1]), qs, m_top)) : 0.f;
                 z2 = add2(z2, pack2(p0, p1));
-                pk[e] = pack_f16(p0, p1);
+                pk[e >> 1] = pack_f16(p0, p1);
               }
-              KVQ_ST8(s_col + 8u * cc, pk);
-            };
-            KVQ_LD16(s0, s_col);
-#pragma unroll 1
-            for (int cc = 0; cc < 8; cc += 2) {
-              tmem_wait_ld();
-              KVQ_LD16(s1, s_col + 16u * cc + 16u);
-              columns(s0, cc);
-              tmem_wait_ld();
-              if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
-              columns(s1, cc + 1);
             }
-          } else {
-#pragma unroll 1
-            for (int cc = 0; cc < 8; ++cc) {
-              const int left = nv - 16 * cc;
-              uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-              if (16 * cc < seen) {
-                uint32_t sr[16];
-                KVQ_LD16(sr, s_col + 16u * cc);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const float p0 = e < left ? ex2(fmaf(__uint_as_float(sr[e]), qs, m_top)) : 0.f;
-                  const float p1 = e + 1 < left ? ex2(fmaf(__uint_as_float(sr[e + 1]), qs, m_top)) : 0.f;
-                  z2 = add2(z2, pack2(p0, p1));
-                  pk[e >> 1] = pack_f16(p0, p1);
-                }
-              }
-              KVQ_ST8(s_col + 8u * cc, pk);
-            }
-          }
-          z += lo_f(z2) + hi_f(z2);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(P_FULL + tile));
-          ++k;
-          end = walk.last(c);
-          if (end) {
-            whole = from_zero && c.j + 1 == c.nb;
-            const int rr = c.it.r0 + tile * TR + r;
-            row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
+            KVQ_ST8(s_col + 8u * cc, pk);
           }
         }
-        if (block) {
-          walk.next(c);
-        }
-        // the next segment's query rows; before this one's own end, so that its
-        // first scores are computed meanwhile
-        if (c.left > 0 && c.start && walk.tiles(c) > tile) {
-          wait(bar(Q_READY + tile), nq & 1u, abort_flag);
-          ++nq;
-          const int2 pw = s_pow[seg & 3u];                 // (written before the rows were asked for)
-          q_next = p.qscale * exp2i(pw.x - kTop) * (r < TR ? row_to_f16<D>(sm + M::kQ + tile * M::kTile, r) : 1.f);
-          ov_next = exp2i(pw.y - kTop);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Q_FP16 + tile));
-        }
-        if (end) {
+        z += lo_f(z2) + hi_f(z2);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P_FULL + tile));
+        ++k;
+        if (walk.last(c)) {
           // the segment's last P V product must be done before O is read
           wait(bar(PV_DONE + tile), (k - 1) & 1u, abort_flag);
           tc_fence_after();
           const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
-          poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
+          const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
+          const bool whole = from_zero && c.j + 1 == c.nb;
           const int pr = tile * 128 + r;
           float* part = p.partials + (2 * static_cast<long long>(blockIdx.x) + (seg_is_first ? 0 : 1)) * 256 * (D + 2) +
                         static_cast<long long>(pr >> 5) * (D + 2) * 32 + (pr & 31);
@@ -909,7 +905,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           }
           tc_fence_before();
         }
-        if (c.left <= 0) break;
       }
     }
   }
@@ -946,9 +941,22 @@ bool applies(const AttendArgs& a) {
 size_t partials_bytes(const AttendArgs& a) {
   return 2 * static_cast<size_t>(ctas(a)) * 256 * (a.g.D + 2) * sizeof(float);
 }
-size_t workspace(const AttendArgs& a) {
-  return plan_bytes(a, item_rows(a)) + partials_bytes(a) + 2 * sizeof(uint32_t) * kParts * a.S * a.g.H_kv;
+// workspace: the plan, partial results, fp16 query rows and their powers, largest scales
+struct Layout {
+  size_t partials, rows, powers, tops, bytes;
+};
+Layout layout(const AttendArgs& a) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t rows = static_cast<size_t>(a.T) * a.H_q;
+  Layout l;
+  l.partials = up(plan_bytes(a, item_rows(a)));
+  l.rows = l.partials + up(partials_bytes(a));
+  l.powers = l.rows + up(rows * a.g.D * 2);
+  l.tops = l.powers + up(rows * sizeof(float));
+  l.bytes = l.tops + 2 * sizeof(uint32_t) * kParts * a.S * a.g.H_kv;
+  return l;
 }
+size_t workspace(const AttendArgs& a) { return layout(a).bytes; }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link)
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -970,7 +978,7 @@ EncodeTiled encode_tiled() {
 // half: 64 features x G heads x 1 x TT tokens, rows token-major in shared
 // memory with the 128-byte swizzle the UMMA descriptors expect.  Tokens past T
 // read as zero.
-bool make_q_map(const AttendArgs& a, CUtensorMap* map) {
+bool make_q_map(const AttendArgs& a, void* rows, CUtensorMap* map) {
   const EncodeTiled enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t D = static_cast<cuuint64_t>(a.g.D), G = static_cast<cuuint64_t>(a.G),
@@ -979,7 +987,7 @@ bool make_q_map(const AttendArgs& a, CUtensorMap* map) {
   const cuuint64_t strides[3] = {D * 2, G * D * 2, H * G * D * 2};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), 1, static_cast<cuuint32_t>(tile_tokens(a))};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.Q), dims, strides, box, estr,
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, rows, dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -987,7 +995,9 @@ bool make_q_map(const AttendArgs& a, CUtensorMap* map) {
 kvq_status launch(const AttendArgs& a, cudaStream_t s) {
   const int RI = item_rows(a);
   CUtensorMap qmap;
-  if (!make_q_map(a, &qmap)) return KVQ_ERR_CUDA;
+  const Layout l = layout(a);
+  char* ws = static_cast<char*>(a.workspace);
+  if (!make_q_map(a, ws + l.rows, &qmap)) return KVQ_ERR_CUDA;
   Params p{};
   p.t = make_batch(a);
   p.plan = plan_mem(a, RI, a.workspace);
@@ -997,9 +1007,15 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
   p.v_scales = a.v_scales;
   p.qscale = a.scale * kLog2e;
   p.O = static_cast<__nv_bfloat16*>(a.O);
-  p.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan_bytes(a, RI));
-  uint32_t* tops = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(p.partials) + partials_bytes(a));
+  p.partials = reinterpret_cast<float*>(ws + l.partials);
+  float* q_pow = reinterpret_cast<float*>(ws + l.powers);
+  uint32_t* tops = reinterpret_cast<uint32_t*>(ws + l.tops);
+  // two CTAs an SM where the sequences and heads alone are fewer
+  const long long bh = static_cast<long long>(a.S) * a.g.H_kv;
+  const int parts = static_cast<int>(std::min<long long>(kParts, std::max<long long>(1, (2 * 148 + bh - 1) / bh)));
   p.tops = tops;
+  p.parts = parts;
+  p.q_pow = q_pow;
   p.ctas = ctas(a);
   p.RI = RI;
   p.TT = tile_tokens(a);
@@ -1009,8 +1025,14 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
     const kvq_status st = launch_plan(a, p.plan, RI, kBT, s);
     if (st != KVQ_OK) return st;
   }
-  if (launch_pdl(a.g.D == 64 ? paged_scales_kernel<64> : paged_scales_kernel<128>, dim3(a.S, a.g.H_kv, kParts),
-                 dim3(32 * kScanWarps), 0, s, p.t, p.k_scales, p.v_scales, tops, p.err) != cudaSuccess)
+  const long long rows = static_cast<long long>(a.T) * a.H_q;
+  const int row_pass = 32 * kPrepareWarps / (a.g.D / 8) * kRowsPerLane;
+  const long long blocks = bh * parts + (rows + row_pass - 1) / row_pass;
+  if (blocks > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  if (launch_pdl(a.g.D == 64 ? paged_prepare_kernel<64> : paged_prepare_kernel<128>,
+                 dim3(static_cast<unsigned>(blocks)), dim3(32 * kPrepareWarps), 0, s, p.t, p.k_scales, p.v_scales, tops,
+                 parts, static_cast<const uint4*>(a.Q), reinterpret_cast<uint4*>(ws + l.rows), q_pow, rows, p.err) !=
+      cudaSuccess)
     return KVQ_ERR_CUDA;
   count_launch();
   const size_t smem = smem_of(a);
