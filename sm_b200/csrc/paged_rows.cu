@@ -413,14 +413,16 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
         }
       }
       // the codes' offset: the operand holds 16 + n (and 256 + 16 n), so each
-      // score is too large by that constant times the sum of q'
-      float cc[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+      // score is too large by that constant times the sum of q' (f32 rows take
+      // it from the operand instead: the larger sums would round away more)
+      corr[n] = 0.f;
+      if (NS == 2) {
+        float cc[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-      for (int set = 0; set < C::SETS; ++set)
-#pragma unroll
-        for (int k = 0; k < D / 8; k += 2) mma(cc, ones, bq[n][set][k], bq[n][set][k + 1]);
-      corr[n] = (BITS == 4 ? -23.f : -399.f) * (cc[0] + cc[1]);
+        for (int k = 0; k < D / 8; k += 2) mma(cc, ones, bq[n][0][k], bq[n][0][k + 1]);
+        corr[n] = (BITS == 4 ? -23.f : -399.f) * (cc[0] + cc[1]);
+      }
     }
 
     // ---- scores of the block: lane = row c of each tile, tokens g + 8 i ------
@@ -452,10 +454,17 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
         for (int k = 0; k < STEP; ++k) {
           const int x = x0 + k;
           if (BITS == 4) {
-            const uint32_t a0[4] = {nibbles<0, false>(wa[k]), nibbles<0, false>(wb[k]), nibbles<1, false>(wa[k]),
-                                    nibbles<1, false>(wb[k])};
-            const uint32_t a1[4] = {nibbles<2, false>(wa[k]), nibbles<2, false>(wb[k]), nibbles<3, false>(wa[k]),
-                                    nibbles<3, false>(wb[k])};
+            uint32_t a0[4] = {nibbles<0, false>(wa[k]), nibbles<0, false>(wb[k]), nibbles<1, false>(wa[k]),
+                              nibbles<1, false>(wb[k])};
+            uint32_t a1[4] = {nibbles<2, false>(wa[k]), nibbles<2, false>(wb[k]), nibbles<3, false>(wa[k]),
+                              nibbles<3, false>(wb[k])};
+            if (NS == 3) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                a0[e] = add_bf16x2(a0[e], 0xC1B8C1B8u);       // -23
+                a1[e] = add_bf16x2(a1[e], 0xC1B8C1B8u);
+              }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -464,10 +473,17 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
                 mma(acc[n], a1, bq[n][set][4 * x + 2], bq[n][set][4 * x + 3]);
               }
           } else {
-            const uint32_t a0[4] = {nibbles<0, false>(wa[k]), nibbles<0, false>(wb[k]), nibbles<2, false>(wa[k]),
-                                    nibbles<2, false>(wb[k])};
-            const uint32_t a1[4] = {nibbles<1, true>(wa[k]), nibbles<1, true>(wb[k]), nibbles<3, true>(wa[k]),
-                                    nibbles<3, true>(wb[k])};
+            uint32_t a0[4] = {nibbles<0, false>(wa[k]), nibbles<0, false>(wb[k]), nibbles<2, false>(wa[k]),
+                              nibbles<2, false>(wb[k])};
+            uint32_t a1[4] = {nibbles<1, true>(wa[k]), nibbles<1, true>(wb[k]), nibbles<3, true>(wa[k]),
+                              nibbles<3, true>(wb[k])};
+            if (NS == 3) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                a0[e] = add_bf16x2(a0[e], 0xC1F8C1F8u);       // -31
+                a1[e] = add_bf16x2(a1[e], 0xC3B8C3B8u);       // -368
+              }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -528,6 +544,19 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
       }
 
     // ---- O^T += V^T p', 16 tokens at a time -----------------------------------
+    // The tensor cores' sums are cut off, not rounded: f32 rows add them to the
+    // running ones outside, rounded, or the loss grows with the length.
+    auto weigh = [](float (&acc)[4], const uint32_t (&a)[4], const uint32_t (&b)[C::SETS][2]) {
+      if (NS == 2) {
+        mma(acc, a, b[0][0], b[0][1]);
+      } else {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int set = C::SETS - 1; set >= 0; --set) mma(x, a, b[set][0], b[set][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += x[e];
+      }
+    };
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const int ta = 16 * hh + g, tb = ta + 8;
@@ -572,12 +601,10 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
           const uint32_t a1[4] = {add_bf16x2(nibbles<2, false>(xr[0]), off), add_bf16x2(nibbles<3, false>(xr[0]), off),
                                   add_bf16x2(nibbles<2, false>(xr[1]), off), add_bf16x2(nibbles<3, false>(xr[1]), off)};
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int set = 0; set < C::SETS; ++set) {
-              mma(u[n][2 * fg], a0, bp[n][set][0], bp[n][set][1]);
-              mma(u[n][2 * fg + 1], a1, bp[n][set][0], bp[n][set][1]);
-            }
+          for (int n = 0; n < NT; ++n) {
+            weigh(u[n][2 * fg], a0, bp[n]);
+            weigh(u[n][2 * fg + 1], a1, bp[n]);
+          }
         } else {
           ldsm4t(xr, st_u + C::kOffV + 16 * v_slot<C::CH>(tr, 2 * fg + (lane >> 4)));
           const uint32_t ol = 0xC1F8C1F8u, ol0 = 0xC30FC30Fu, oh = 0xC3B8C3B8u;   // -31, -143, -368
@@ -589,12 +616,10 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
             const uint32_t a1[4] = {add_bf16x2(nibbles<1, true>(xa), oh), add_bf16x2(nibbles<3, true>(xa), oh),
                                     add_bf16x2(nibbles<1, true>(xb), oh), add_bf16x2(nibbles<3, true>(xb), oh)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int set = 0; set < C::SETS; ++set) {
-                mma(u[n][2 * fg + k], a0, bp[n][set][0], bp[n][set][1]);
-                mma(u[n][2 * fg + k], a1, bp[n][set][0], bp[n][set][1]);
-              }
+            for (int n = 0; n < NT; ++n) {
+              weigh(u[n][2 * fg + k], a0, bp[n]);
+              weigh(u[n][2 * fg + k], a1, bp[n]);
+            }
           }
         }
       }
