@@ -315,8 +315,11 @@ constexpr int kPrepareWarps = 8, kRowsPerLane = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kPrepareWarps)
     paged_prepare_kernel(Batch t, const float* k_scales, const float* v_scales, uint32_t* tops, int parts,
-                         const uint4* Q, uint4* Qh, float* q_pow, long long rows, unsigned int* err) {
-  griddep_wait();
+                         const uint4* Q, uint4* Qh, float* q_pow, long long rows, int beside, unsigned int* err) {
+  // beside: the kernel before is the plan's, which has waited for every other
+  // and writes what this one does not touch
+  if (beside) griddep_release();
+  else griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long scans = static_cast<long long>(t.S) * t.H * parts;
   if (blockIdx.x >= scans) {
@@ -348,6 +351,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
         if (l == 0) q_pow[row] = exp2i(e - kTopQ);
       }
     }
+    if (beside) griddep_join();
     return;
   }
   const int part = static_cast<int>(blockIdx.x % parts), bh = static_cast<int>(blockIdx.x / parts);
@@ -398,6 +402,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
     for (int w = 0; w < kPrepareWarps; ++w) m = max(m, s_top[threadIdx.x][w]);
     tops[(static_cast<long long>(bh) * 2 + threadIdx.x) * kParts + part] = m;
   }
+  if (beside) griddep_join();
 }
 
 template <int BITS, int D>
@@ -758,13 +763,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
           m_ref = -INFINITY;
           z = 0.f;
-          qs = real ? p.qscale * __ldcg(p.q_pow + row) : 0.f;   // (no row: equal scores, never a new reference)
+          qs = real ? __ldcg(p.q_pow + row) : 0.f;        // (no row: equal scores, never a new reference)
         }
         if (walk.tiles(c) <= tile) continue;
         wait(bar(S_FULL + tile), k & 1u, abort_flag);
         if (c.start) {                                    // (written before the query rows were asked for)
           const int2 pw = s_pow[(seg - 1) & 3u];
-          qs *= exp2i(pw.x - kTop);
+          qs = p.qscale * qs * exp2i(pw.x - kTop);
           ov = exp2i(pw.y - kTop);
         }
         tc_fence_after();
@@ -1010,9 +1015,9 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
   p.partials = reinterpret_cast<float*>(ws + l.partials);
   float* q_pow = reinterpret_cast<float*>(ws + l.powers);
   uint32_t* tops = reinterpret_cast<uint32_t*>(ws + l.tops);
-  // two CTAs an SM where the sequences and heads alone are fewer
+  // four CTAs an SM where the sequences and heads alone are fewer
   const long long bh = static_cast<long long>(a.S) * a.g.H_kv;
-  const int parts = static_cast<int>(std::min<long long>(kParts, std::max<long long>(1, (2 * 148 + bh - 1) / bh)));
+  const int parts = static_cast<int>(std::min<long long>(kParts, std::max<long long>(1, (4 * 148 + bh - 1) / bh)));
   p.tops = tops;
   p.parts = parts;
   p.q_pow = q_pow;
@@ -1031,7 +1036,8 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
   if (blocks > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
   if (launch_pdl(a.g.D == 64 ? paged_prepare_kernel<64> : paged_prepare_kernel<128>,
                  dim3(static_cast<unsigned>(blocks)), dim3(32 * kPrepareWarps), 0, s, p.t, p.k_scales, p.v_scales, tops,
-                 parts, static_cast<const uint4*>(a.Q), reinterpret_cast<uint4*>(ws + l.rows), q_pow, rows, p.err) !=
+                 parts, static_cast<const uint4*>(a.Q), reinterpret_cast<uint4*>(ws + l.rows), q_pow, rows, p.plan.count != nullptr,
+                 p.err) !=
       cudaSuccess)
     return KVQ_ERR_CUDA;
   count_launch();
