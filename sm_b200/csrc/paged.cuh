@@ -153,13 +153,17 @@ __device__ __forceinline__ int item_blocks(const Batch& t, const SeqView& s, int
   return (row_limit(t, s, last) + BT - 1) / BT;
 }
 
-// Largest item i with H * pre[i] <= g.
+// Largest item i with H * pre[i] <= g; by a whole warp, 32 probes a round.
 __device__ __forceinline__ int find_item(const PlanView& v, int H, long long g) {
-  int lo = 0, hi = v.items - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(H) * v.pre[mid] <= g) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = v.items;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const bool le = at < n && static_cast<long long>(H) * v.pre[lo + at] <= g;
+    const int k = __popc(__ballot_sync(0xffffffffu, le));
+    if (k == 0) break;
+    lo += (k - 1) * step;
+    n = min(step, n - (k - 1) * step);
   }
   return lo;
 }

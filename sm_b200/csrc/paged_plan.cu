@@ -120,6 +120,7 @@ struct Parts {
 // Where there are more (item, head)s than workers, the units are the
 // boundaries between workers: the first boundary inside an (item, head)
 // merges it, and the many that one worker covers cost nothing.
+// (By a whole warp.)
 __device__ __forceinline__ Parts find_parts(const MergeParams& p, const PlanView& v, int unit) {
   const MergeCall& c = p.c;
   const int H = c.t.H;
@@ -174,7 +175,7 @@ __device__ __forceinline__ float exp2_w(float x) {
   return y;
 }
 
-// The plan, the unit's parts (computed by one thread: its 64-bit divisions run
+// The plan, the unit's parts (computed by one warp: their 64-bit divisions run
 // once per CTA) and the wait for the attention kernel.  The inline plan reads
 // only the call's inputs (through the L2), so it runs while that kernel
 // drains; the workspace's plan is read after the wait.
@@ -184,10 +185,9 @@ __device__ __forceinline__ PlanView merge_prologue(const MergeParams& p, int uni
   if (threadIdx.x < 32) {
     if (!global) warp_prefix(p.c.t, p.c.RI, p.c.BT, s_pre);
     __syncwarp();
-    if (threadIdx.x == 0) {
-      *s_parts = Parts{};
-      if (unit < p.units) *s_parts = find_parts(p, plan_view(p.c.plan, s_pre, p.c.t.S), unit);
-    }
+    Parts q{};
+    if (unit < p.units) q = find_parts(p, plan_view(p.c.plan, s_pre, p.c.t.S), unit);
+    if (threadIdx.x == 0) *s_parts = q;
   }
   __syncthreads();
   if (!global) griddep_wait();
@@ -308,33 +308,36 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(MergeParam
   }
 }
 
-// Feature-major partials: one CTA per unit, 32-row chunk (blockIdx.y) and 32
-// features (blockIdx.z); lane = row, a warp takes four features, four parts'
-// loads in flight.
+// Feature-major partials: one CTA per unit and 32-row chunk (blockIdx.y); lane =
+// row, a warp takes D / 8 features, four at a time, two parts' loads in flight.
+// (With a CTA for 32 features each, the unit's parts were looked for four times
+// as often: five prompts took 397 instead of 385 us.)
+template <int D>
 __global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
   extern __shared__ int s_pre[];
   __shared__ Parts s_parts;
   const MergeCall& c = p.c;
   const PlanView v = merge_prologue(p, blockIdx.x, s_pre, &s_parts);
   if (static_cast<int>(blockIdx.x) >= p.units) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) odd_jobs(p, v, blockIdx.x - p.units, gridDim.x - p.units);
+    if (blockIdx.y == 0) odd_jobs(p, v, blockIdx.x - p.units, gridDim.x - p.units);
     return;
   }
   const Parts q = s_parts;
   if (!q.mine) return;
-  const int lane = threadIdx.x & 31, f = 32 * blockIdx.z + 4 * (threadIdx.x >> 5);
+  constexpr int F = D / 8, PB = 2;
+  const int lane = threadIdx.x & 31, f = F * (threadIdx.x >> 5);
   const int pr = 32 * blockIdx.y + lane, tile = pr >> 7;               // padded row of the slot
   const int r = tile * c.tile_rows + (pr & 127);
   const bool real = (pr & 127) < c.tile_rows && r < q.rows;
   if (!__any_sync(0xffffffffu, real)) return;
-  const int D = c.D;
   const long long stride = 256LL * (D + 2);
   const float* base = c.partials + static_cast<long long>(blockIdx.y) * (D + 2) * 32 + lane;
-  float M = -INFINITY, Z = 0.f, U[4] = {0.f, 0.f, 0.f, 0.f};
-  constexpr int PB = 4;
+  float M = -INFINITY, Z = 0.f, U[F];
+#pragma unroll
+  for (int e = 0; e < F; ++e) U[e] = 0.f;
   bool nan = false;
   for (int k0 = 0; k0 < q.n; k0 += PB) {
-    float m[PB], z[PB], u[PB][4];
+    float m[PB], z[PB], u[PB][F];
 #pragma unroll
     for (int k = 0; k < PB; ++k) {
       m[k] = -INFINITY;
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
         m[k] = part[0];
         z[k] = part[32];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[k][e] = part[(2 + f + e) * 32];
+        for (int e = 0; e < F; ++e) u[k][e] = part[(2 + f + e) * 32];
       }
     }
     float top = M;
@@ -358,22 +361,30 @@ __global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
     M = top;
     Z *= keep;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) U[e] *= keep;
+    for (int e = 0; e < F; ++e) U[e] *= keep;
 #pragma unroll
     for (int k = 0; k < PB; ++k)
       if (z[k] > 0.f) {
         const float w = exp2_w(m[k] - top);
         Z = fmaf(w, z[k], Z);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) U[e] = fmaf(w, u[k][e], U[e]);
+        for (int e = 0; e < F; ++e) U[e] = fmaf(w, u[k][e], U[e]);
       }
   }
   if (real) {
     const long long o = out_row(c, q, r) * D + f;
     const float inv = nan ? NAN : (Z > 0.f ? 1.f / Z : 0.f);
-    __nv_bfloat162 lo = __floats2bfloat162_rn(U[0] * inv, U[1] * inv), hi = __floats2bfloat162_rn(U[2] * inv, U[3] * inv);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(c.O) + o) =
-        make_uint2(*reinterpret_cast<unsigned*>(&lo), *reinterpret_cast<unsigned*>(&hi));
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.O) + o);
+#pragma unroll
+    for (int e = 0; e < F; e += 8) {
+      unsigned x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(U[e + 2 * i] * inv, U[e + 2 * i + 1] * inv);
+        x[i] = *reinterpret_cast<const unsigned*>(&b);
+      }
+      dst[e / 8] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
   }
 }
 
@@ -405,10 +416,11 @@ kvq_status launch_merge(const MergeCall& c, cudaStream_t s) {
   const size_t smem = c.plan.count ? 0 : (static_cast<size_t>(c.t.S) + 1) * sizeof(int);
   cudaError_t e;
   if (c.tile_rows > 0) {
-    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(merge_tiles_kernel), smem)) return KVQ_ERR_CUDA;
+    auto kernel = c.D == 64 ? merge_tiles_kernel<64> : merge_tiles_kernel<128>;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
     const int tiles = c.RI > c.tile_rows ? 2 : 1;
     const int last = c.RI - (tiles - 1) * c.tile_rows;                 // rows of the last tile
-    e = launch_pdl(merge_tiles_kernel, dim3(gx, 4 * (tiles - 1) + (last + 31) / 32, c.D / 32), dim3(256), smem, s, p);
+    e = launch_pdl(kernel, dim3(gx, 4 * (tiles - 1) + (last + 31) / 32), dim3(256), smem, s, p);
   } else {
     auto kernel = c.D % 4 == 0 ? merge_rows_kernel<true> : merge_rows_kernel<false>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
