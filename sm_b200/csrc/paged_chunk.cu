@@ -91,7 +91,7 @@ struct Smem {
   static constexpr int kRing = kV + kTile;
   static constexpr int kRingBytes = 55 * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 54 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
+  static constexpr int kMisc = kBar + 58 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
   static constexpr int kPow = kMisc + 80;          // int2 [4]: a segment's exponents (K, V)
   static constexpr int kPre = kPow + 32;            // int pre[S + 1] (inline plan)
 };
@@ -103,12 +103,12 @@ enum Bar {
   K_FREE = 38,                   // [2]
   V_READY = 40,
   V_FREE = 41,
-  S_FULL = 42,                   // [2]
-  P_FULL = 44,                   // [2]
-  PV_DONE = 46,                  // [2]
-  Q_READY = 48,
-  Q_FREE = 49,
-  POWERS = 50,                   // [4]
+  S_FULL = 42,                   // [3]: tile 0, tile 1, a lone tile's other S / P
+  P_FULL = 45,                   // [3]
+  PV_DONE = 48,                  // [3]
+  Q_READY = 51,
+  Q_FREE = 52,
+  POWERS = 53,                   // [4]
 };
 
 struct Params {
@@ -439,6 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(K_READY + i), kDecodeWarps);
       mbar_init(bar(K_FREE + i), 1);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(bar(S_FULL + i), 1);
       mbar_init(bar(P_FULL + i), 4);
       mbar_init(bar(PV_DONE + i), 1);
@@ -564,31 +566,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       // descriptors: the address field counts 16-byte units, so a step adds to the low word
       const uint64_t dq = smem_desc(base + M::kQ, 16, 1024), dk = smem_desc(base + M::kK, 16, 1024),
                      dv = smem_desc(base + M::kV, kTileHalf, 1024);
-      auto qk = [&](int t, uint32_t k) {
-        const uint64_t q0 = dq + static_cast<uint64_t>(t * (M::kTile >> 4)),
+      // u: 0 and 1, the tiles; 2, a lone tile's other S / P (in tile 1's columns)
+      auto qk = [&](int u, uint32_t k) {
+        const uint64_t q0 = dq + static_cast<uint64_t>((u & 1) * (M::kTile >> 4)),
                        k0 = dk + static_cast<uint64_t>((k & 1u) * (M::kTile >> 4));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint64_t step = static_cast<uint64_t>(((i >> 2) * kTileHalf + (i & 3) * 32) >> 4);
-          mma_ss_if(lead, tm + 128u * t, q0 + step, k0 + step, idesc_qk, i > 0);
+          mma_ss_if(lead, tm + (u > 0 ? 128u : 0u), q0 + step, k0 + step, idesc_qk, i > 0);
         }
-        mma_commit_if(lead, bar(S_FULL + t));
+        mma_commit_if(lead, bar(S_FULL + u));
       };
-      uint32_t done[2] = {0, 0};                          // P V products issued per tile
-      auto pv = [&](int t, bool first) {
-        wait(bar(P_FULL + t), done[t] & 1u, abort_flag);
+      uint32_t done[3] = {0, 0, 0};                       // P V products issued
+      auto pv = [&](int u, bool first) {
+        wait(bar(P_FULL + u), done[u] & 1u, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < kBT / 16; ++i)
-          mma_ts_if(lead, tm + 256u + 128u * t, tm + 128u * t + 8u * i, dv + static_cast<uint64_t>(i * 128), idesc_pv,
-                    (!first) || (i > 0));
-        mma_commit_if(lead, bar(PV_DONE + t));
-        ++done[t];
+          mma_ts_if(lead, tm + 256u + 128u * (u & 1), tm + (u > 0 ? 128u : 0u) + 8u * i,
+                    dv + static_cast<uint64_t>(i * 128), idesc_pv, (!first) || (i > 0));
+        mma_commit_if(lead, bar(PV_DONE + u));
+        ++done[u];
       };
-      // S of a tile overwrites its P: the last P V product must be done
-      auto pv_done = [&](int t) {
-        if (done[t] > 0) {
-          wait(bar(PV_DONE + t), (done[t] - 1) & 1u, abort_flag);
+      // an S overwrites the P there: the last P V product must be done
+      auto pv_done = [&](int u) {
+        if (done[u] > 0) {
+          wait(bar(PV_DONE + u), (done[u] - 1) & 1u, abort_flag);
           tc_fence_after();
         }
       };
@@ -603,14 +606,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         return __shfl_sync(0xffffffffu, f, 0);
       };
       uint32_t sq = 0;                                    // segments begun
+      bool other = false, other_next = false;             // the current block's S is a lone tile's other one
       uint32_t fc = 0, fn = 0;                            // the current block's (k) and the next one's
 #pragma unroll 1
       for (uint32_t k = ~0u - 1u;; ++k) {                 // (the first rounds have no current block, no next one)
         const bool have = fc & kMore, more = fn & kMore, boundary = more && (fn & kStart);
+        // a lone tile has its S twice: the next block's scores are there before
+        // this one's values are
+        const bool lone = have && more && !boundary && !(fn & kTwo);
+        if (boundary) other_next = false;
+        else other_next = !other && !(fn & kTwo);
+        if (lone) {
+          wait(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, abort_flag);
+          if (other_next) {
+            pv_done(1);
+            pv_done(2);
+            tc_fence_after();
+            qk(2, k + 1);
+          } else {
+            pv_done(0);
+            tc_fence_after();
+            qk(0, k + 1);
+          }
+          mma_commit_if(lead, bar(K_FREE + ((k + 1) & 1u)));
+          if (fn & kLast) mma_commit_if(lead, bar(Q_FREE));
+        }
         if (have) {
           wait(bar(V_READY), k & 1u, abort_flag);
           tc_fence_after();
-          pv(0, fc & kStart);
+          if (other) pv(2, fc & kStart);
+          else pv(0, fc & kStart);
         }
         const uint32_t fnn = flags();                     // while the product runs
         // Q K of the next block's first tile, then P V of this one's second; the
@@ -618,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 1
         for (int step = 0; step < 2; ++step) {
           if (step == boundary) {
-            if (more) {
+            if (more && !lone) {
               if (boundary) wait(bar(Q_READY), sq++ & 1u, abort_flag);
               wait(bar(K_READY + ((k + 1) & 1u)), ((k + 1) >> 1) & 1u, abort_flag);
               pv_done(0);
@@ -630,9 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
             mma_commit_if(lead, bar(V_FREE));
           }
         }
-        if (more) {
+        if (more && !lone) {
           if (fn & kTwo) {
             pv_done(1);
+            pv_done(2);
             tc_fence_after();
             qk(1, k + 1);
           }
@@ -641,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
         fc = fn;
         fn = fnn;
+        other = other_next;
         if (!(fc | fn)) break;
       }
       __syncwarp();
@@ -740,12 +767,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       const int tile = (warp - 4) >> 2;
       const int r = ((warp & 3) << 5) + lane;            // TMEM lane = row within the tile
       const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t s_col = tmem + lane_addr + 128u * tile;
       const uint32_t o_col = tmem + lane_addr + 256u + 128u * tile;
       const bool neg = p.qscale < 0.f;
       float m_ref = -INFINITY, z = 0.f;
       float qs = 0.f, ov = 0.f;                           // what the row's scores and its O are multiplied by
-      uint32_t k = 0, seg = 0;                            // blocks of this tile, segments of the CTA
+      uint32_t k[2] = {0, 0}, seg = 0;                    // blocks of the tile's S and of its other one; segments of the CTA
+      bool other = true;
       long long row = 0;                                  // of Q and O
       int lim = 0;                                        // keys the row sees
       bool real = false;                                  // the row exists
@@ -765,8 +792,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           z = 0.f;
           qs = real ? __ldcg(p.q_pow + row) : 0.f;        // (no row: equal scores, never a new reference)
         }
-        if (walk.tiles(c) <= tile) continue;
-        wait(bar(S_FULL + tile), k & 1u, abort_flag);
+        const bool lone = walk.tiles(c) == 1;
+        if (lone && tile) continue;
+        other = lone && !c.start && !other;               // a lone tile takes its two in turn
+        const int u = other ? 2 : tile;
+        const uint32_t s_col = tmem + lane_addr + (u > 0 ? 128u : 0u), nth = other ? k[1] : k[0];
+        wait(bar(S_FULL + u), nth & 1u, abort_flag);
         if (c.start) {                                    // (written before the query rows were asked for)
           const int2 pw = s_pow[(seg - 1) & 3u];
           qs = p.qscale * qs * exp2i(pw.x - kTop);
@@ -805,6 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
           if (need) m_ref = mb;
           z *= a;
           if (!c.start) {
+            if (lone) {                                   // (its S did not wait for the last product)
+              wait(bar(PV_DONE + 2 - u), ((other ? k[0] : k[1]) - 1) & 1u, abort_flag);
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int oc = 0; oc < D / 16; ++oc) {
               uint32_t orr[16];
@@ -868,11 +903,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P_FULL + tile));
-        ++k;
+        if (lane == 0) mbar_arrive(bar(P_FULL + u));
+        if (other) ++k[1]; else ++k[0];
         if (walk.last(c)) {
           // the segment's last P V product must be done before O is read
-          wait(bar(PV_DONE + tile), (k - 1) & 1u, abort_flag);
+          wait(bar(PV_DONE + u), nth & 1u, abort_flag);
           tc_fence_after();
           const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
           const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;

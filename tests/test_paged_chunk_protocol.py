@@ -4,8 +4,9 @@ copies and MMAs that complete out of order, a version on every buffer).
 
 What differs from the contiguous kernel: the ring holds half-units of 64 keys,
 each decoded by four of the eight decode warps; a segment's item has one or two
-row tiles, so the second tile's barriers count its own blocks; and the Q loader
-leaves a segment's powers of two, four segments deep, to the decode warps and
+row tiles, so the second tile's barriers count its own blocks; a lone tile has
+its scores in both tiles' columns in turn, with barriers of their own for the
+second, and its next scores before its values; and the Q loader leaves a segment's powers of two, four segments deep, to the decode warps and
 the softmax.  A ring of odd length gives a slot to the two halves in turn,
 and a decode warp sees only its own half's uses of it: the slot's full barrier
 is one per half, since on a shared one a warp would wait for a phase without
@@ -29,6 +30,7 @@ class PagedModel(Model):
                 self.B[("RF", u, half)] = Bar(1)
         for i in range(DEEP):
             self.B[("X", i)] = Bar(1)
+        self.B[("SF", 2)], self.B[("PF", 2)], self.B[("PD", 2)] = Bar(1), Bar(RW), Bar(1)
 
 
 def roles_of(m, drop=None, shift=None, shared_full=False):
@@ -48,8 +50,17 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
         segs[-1].append(b)
     seg_blocks = [[i for i, b in enumerate(blocks) if b[0] == s[0][0]] for s in segs]
     tiles = [b[3] for b in blocks]
-    # a tile's own count of the blocks before k
-    nth = [[sum(1 for x in tiles[:k] if x > t) for k in range(nb)] for t in range(2)]
+    # what a tile uses in a block: 0 and 1, the tiles; 2, a lone tile's other S
+    use = []
+    for k, b in enumerate(blocks):
+        use.append([0, 1] if b[3] == 2 else [0 if b[1] else 2 - use[-1][0]])
+
+    def nth(u, k):
+        return sum(1 for x in use[:k] if u in x)
+
+    def tile_at(u, k):
+        """The tile whose block k's S is in the columns of u."""
+        return 0 if tiles[k] == 1 else min(u, 1)
     units = [("K", 0)]
     for v in range(nb):
         if v + 1 < nb:
@@ -108,21 +119,26 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
             n += 2
             count[typ] += 1
 
-    def qk(t, k):
+    def qk(u, k):
+        t, at = u & 1, min(u, 1)
+
         def fn():
             m.read("Q", next(i for i, s in enumerate(seg_blocks) if k in s), ("qk", t, k))
             for w in range(DW):
                 m.read(("K", k & 1, w), k, ("qk", t, k))
-            m.write(("S", t), k, lambda p: {("pv", t, p)} | {("sm", t, p, w) for w in range(RW)})
-        return [("mma", ("S", t), fn), ("commit", ("SF", t))]
+            m.write(("S", at), k, lambda p: {("pv", tile_at(at, p), p)} | {
+                ("sm", tile_at(at, p), p, w) for w in range(RW)})
+        return [("mma", ("S", at), fn), ("commit", ("SF", u))]
 
-    def pv(t, k):
+    def pv(u, k):
+        t, at = u & 1, min(u, 1)
+
         def fn():
             for w in range(RW):
-                m.read(("P", t, w), k, ("pv", t, k))
+                m.read(("P", at, w), k, ("pv", t, k))
             for w in range(DW):
                 m.read(("V", 0, w), k, ("pv", t, k))
-            m.reads.setdefault(("S", t), set()).add(("pv", t, k))
+            m.reads.setdefault(("S", at), set()).add(("pv", t, k))
             for w in range(RW):
                 o = ("O", t, w)
                 if blocks[k][1]:
@@ -132,72 +148,80 @@ def roles_of(m, drop=None, shift=None, shared_full=False):
                     assert m.buf.get(o) == k - 1, f"P V({k}) accumulates onto O v{m.buf.get(o)}"
                 m.buf[o] = k
                 m.reads[o] = set()
-        return [("mma", ("O", t), fn), ("commit", ("PD", t))]
+        return [("mma", ("O", t), fn), ("commit", ("PD", u))]
 
     def mma():
-        done = [0, 0]
+        done = [0, 0, 0]
 
-        def product(t, k):
-            yield from wait("p_full", ("PF", t), done[t])
-            yield from pv(t, k)
-            done[t] += 1
+        def product(u, k):
+            yield from wait("p_full", ("PF", u), done[u])
+            yield from pv(u, k)
+            done[u] += 1
 
-        def pv_done(t):
-            if done[t] > 0:
-                yield from wait("pv_done", ("PD", t), done[t] - 1)
+        def pv_done(u):
+            for x in ([0] if u == 0 else [1, 2]):
+                if done[x] > 0:
+                    yield from wait("pv_done", ("PD", x), done[x] - 1)
 
-        yield from wait("q_ready", "QR", 0)
-        sq = 1
-        yield from wait("k_ready", ("KR", 0), 0)
-        for t in range(tiles[0]):
-            yield from qk(t, 0)
-        yield ("commit", ("KF", 0))
-        if blocks[0][2]:
-            yield ("commit", "QF")
-        for k in range(nb):
-            nxt = k + 1 < nb
+        def scores(u, k):
+            yield from pv_done(u)
+            yield from qk(u, k)
+
+        def freed(k):
+            yield ("commit", ("KF", k & 1))
+            if blocks[k][2]:
+                yield ("commit", "QF")
+
+        sq = 0
+        for k in range(-1, nb):
+            have, nxt = k >= 0, k + 1 < nb
             boundary = nxt and blocks[k + 1][1]
-            yield from wait("v_ready", "VR", k)
-            yield from product(0, k)
-            if nxt and not boundary:
+            lone = have and nxt and not boundary and tiles[k + 1] == 1
+            if lone:
                 yield from wait("k_ready", ("KR", (k + 1) & 1), (k + 1) >> 1)
-                yield from pv_done(0)
-                yield from qk(0, k + 1)
-            if tiles[k] == 2:
-                yield from product(1, k)
-            yield ("commit", "VF")
-            if nxt:
-                if boundary:
-                    yield from wait("q_ready", "QR", sq)
-                    sq += 1
-                    yield from wait("k_ready", ("KR", (k + 1) & 1), (k + 1) >> 1)
-                    yield from pv_done(0)
-                    yield from qk(0, k + 1)
+                yield from scores(use[k + 1][0], k + 1)
+                yield from freed(k + 1)
+            if have:
+                yield from wait("v_ready", "VR", k)
+                yield from product(use[k][0], k)
+            for step in range(2):
+                if step == boundary:
+                    if nxt and not lone:
+                        if boundary:
+                            yield from wait("q_ready", "QR", sq)
+                            sq += 1
+                        yield from wait("k_ready", ("KR", (k + 1) & 1), (k + 1) >> 1)
+                        yield from scores(0, k + 1)
+                elif have:
+                    if tiles[k] == 2:
+                        yield from product(1, k)
+                    yield ("commit", "VF")
+            if nxt and not lone:
                 if tiles[k + 1] == 2:
-                    yield from pv_done(1)
-                    yield from qk(1, k + 1)
-                yield ("commit", ("KF", (k + 1) & 1))
-                if blocks[k + 1][2]:
-                    yield ("commit", "QF")
+                    yield from scores(1, k + 1)
+                yield from freed(k + 1)
 
     def softmax(t, w):
         for k in range(nb):
             if tiles[k] <= t:
                 continue
-            n = nth[t][k]
-            yield from wait("s_full", ("SF", t), n)
+            u = use[k][t]
+            n = nth(u, k)
+            yield from wait("s_full", ("SF", u), n)
+            if tiles[k] == 1 and not blocks[k][1]:          # (as if O were rescaled every time)
+                yield from wait("rescale", ("PD", 2 - u), nth(2 - u, k) - 1)
 
-            def f(k=k):
-                m.read(("S", t), k, ("sm", t, k, w))
+            def f(k=k, u=u):
+                m.read(("S", min(u, 1)), k, ("sm", t, k, w))
                 if blocks[k][1]:
                     m.read(("X", blocks[k][0] % DEEP), blocks[k][0], ("sm", t, w))
-                if not blocks[k][1]:
+                else:
                     assert m.buf.get(("O", t, w)) == k - 1, "rescale before the previous P V finished"
-                m.buf[("P", t, w)] = k
+                m.buf[("P", min(u, 1), w)] = k
             yield ("do", f)
-            yield ("arrive", ("PF", t))
+            yield ("arrive", ("PF", u))
             if blocks[k][2]:
-                yield from wait("epilogue_pv", ("PD", t), n)
+                yield from wait("epilogue_pv", ("PD", u), n)
                 yield ("do", lambda k=k: m.read(("O", t, w), k, ("epi", t, k)))
 
     roles = {"producer": producer(), "q": qloader(), "mma": mma()}
@@ -215,7 +239,8 @@ def block_list(segments):
 
 
 SEGMENTS = [[(1, 1)], [(1, 2)], [(3, 2)], [(28, 2)], [(5, 2), (23, 2)], [(1, 1), (1, 2), (1, 1), (1, 2)],
-            [(27, 2), (1, 1)], [(1, 2), (27, 1)], [(2, 2), (2, 1), (2, 2), (2, 1), (3, 2)], [(13, 1), (14, 1)]]
+            [(27, 2), (1, 1)], [(1, 2), (27, 1)], [(2, 2), (2, 1), (2, 2), (2, 1), (3, 2)], [(13, 1), (14, 1)],
+            [(4, 1), (2, 2), (5, 1), (1, 2), (1, 1), (7, 1)]]
 
 
 @pytest.mark.parametrize("segments", SEGMENTS, ids=lambda s: "-".join(f"{n}x{t}" for n, t in s))
@@ -227,7 +252,7 @@ def test_protocol_holds(segments, n_units):
 
 
 @pytest.mark.parametrize("drop", ["ring_empty", "q_free", "k_free", "v_free", "pv_done", "epilogue_pv",
-                                  "p_full", "v_ready", "k_ready", "s_full", "powers"])
+                                  "p_full", "v_ready", "k_ready", "s_full", "powers", "rescale"])
 def test_every_wait_is_needed(drop):
     for segments in ([(3, 2)], [(5, 2), (23, 2)], [(27, 2), (1, 1)], [(9, 1), (9, 2), (9, 1)]):
         for seed in range(60):
@@ -244,7 +269,7 @@ def test_every_wait_is_needed(drop):
 def test_every_phase_is_right(shift):
     with pytest.raises(AssertionError):
         for seed in range(10):
-            m = PagedModel(block_list([(5, 2), (23, 2)]), 3, seed, lag=0.3)
+            m = PagedModel(block_list([(5, 2), (18, 1), (5, 2)]), 3, seed, lag=0.3)
             m.run(roles_of(m, shift=shift))
 
 
