@@ -426,6 +426,25 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
     }
 
     // ---- scores of the block: lane = row c of each tile, tokens g + 8 i ------
+    // The tensor cores' sums are cut off, not rounded: f32 rows add them up
+    // outside, rounded, a word's at a time, or the loss grows with D (and, below,
+    // with the length).
+    auto products = [](float (&acc)[4], const uint32_t (&a0)[4], const uint32_t (&a1)[4],
+                       const uint32_t (&b)[C::SETS][D / 8], int j0, int j1) {
+      if (NS == 2) {
+        mma(acc, a0, b[0][j0], b[0][j0 + 1]);
+        mma(acc, a1, b[0][j1], b[0][j1 + 1]);
+      } else {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int set = C::SETS - 1; set >= 0; --set) {
+          mma(x, a0, b[set][j0], b[set][j0 + 1]);
+          mma(x, a1, b[set][j1], b[set][j1 + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += x[e];
+      }
+    };
     float sc[NT][4];
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -466,12 +485,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
               }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int set = 0; set < C::SETS; ++set) {
-                mma(acc[n], a0, bq[n][set][4 * x], bq[n][set][4 * x + 1]);
-                mma(acc[n], a1, bq[n][set][4 * x + 2], bq[n][set][4 * x + 3]);
-              }
+            for (int n = 0; n < NT; ++n) products(acc[n], a0, a1, bq[n], 4 * x, 4 * x + 2);
           } else {
             uint32_t a0[4] = {nibbles<0, false>(wa[k]), nibbles<0, false>(wb[k]), nibbles<2, false>(wa[k]),
                               nibbles<2, false>(wb[k])};
@@ -485,12 +499,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
               }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int set = 0; set < C::SETS; ++set) {
-                mma(acc[n], a0, bq[n][set][2 * x], bq[n][set][2 * x + 1]);
-                mma(acc[n], a1, bq[n][set][2 * x], bq[n][set][2 * x + 1]);
-              }
+            for (int n = 0; n < NT; ++n) products(acc[n], a0, a1, bq[n], 2 * x, 2 * x);
           }
         }
       }
@@ -544,8 +553,6 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
       }
 
     // ---- O^T += V^T p', 16 tokens at a time -----------------------------------
-    // The tensor cores' sums are cut off, not rounded: f32 rows add them to the
-    // running ones outside, rounded, or the loss grows with the length.
     auto weigh = [](float (&acc)[4], const uint32_t (&a)[4], const uint32_t (&b)[C::SETS][2]) {
       if (NS == 2) {
         mma(acc, a, b[0][0], b[0][1]);
