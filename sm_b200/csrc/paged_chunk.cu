@@ -974,9 +974,12 @@ size_t smem_of(const AttendArgs& a) { return a.g.D == 64 ? smem_bytes<64>(a) : s
 
 int ctas(const AttendArgs& a) { return a.splits > 0 ? a.splits : (sm_count() > 0 ? sm_count() : 148); }
 
+// Below these rows a KV head the rows kernel is faster (16 sequences of 4096 keys,
+// D = 128, us: rows / this one): 4 bits 8 rows 43 / 88, 16 rows 81 / 89, 20 rows
+// 110 / 89; 8 bits 8 rows 59 / 87, 9 rows 106 / 87 (the rows kernel's second tile).
 bool applies(const AttendArgs& a) {
   return a.g.group == 32 && (a.g.D == 64 || a.g.D == 128) && a.q_dtype == KVQ_BF16 && a.G <= 128 &&
-         static_cast<long long>(a.max_q) * a.G > 16 && smem_of(a) <= 227 * 1024;
+         static_cast<long long>(a.max_q) * a.G > (a.g.bits == 4 ? 16 : 8) && smem_of(a) <= 227 * 1024;
 }
 size_t partials_bytes(const AttendArgs& a) {
   return 2 * static_cast<size_t>(ctas(a)) * 256 * (a.g.D + 2) * sizeof(float);

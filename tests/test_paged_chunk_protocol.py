@@ -244,7 +244,7 @@ SEGMENTS = [[(1, 1)], [(1, 2)], [(3, 2)], [(28, 2)], [(5, 2), (23, 2)], [(1, 1),
 
 
 @pytest.mark.parametrize("segments", SEGMENTS, ids=lambda s: "-".join(f"{n}x{t}" for n, t in s))
-@pytest.mark.parametrize("n_units", [3, 5, 11, 12])
+@pytest.mark.parametrize("n_units", [3, 6, 11, 12])
 def test_protocol_holds(segments, n_units):
     for seed in range(10):
         m = PagedModel(block_list(segments), n_units, seed, lag=(seed % 4) * 0.3)
