@@ -13,7 +13,16 @@
 // shared memory, so each new K and V element is read once.  The group that a
 // call begins in reads the tail slot and the group that it ends in writes it;
 // where these are two groups and both are unfinished, one CTA does them one
-// after the other, so the slot's rows are read before they are replaced.
+// after the other, so the slot's rows are read before they are replaced.  The
+// vector form (features in eights, groups a power of two) gives K and V a CTA
+// each, eight features a lane; a call of one token a sequence has V in K's.
+//
+// Bound by memory where the call is large, by latency where it is small.  8
+// thousand new tokens of 8 heads, D = 128, and reading 8 thousand back: 140 MB in
+// 69 us (2.0 TB/s; append 32, gather 27); one token of each of 64 sequences, and
+// as many read back: 17 us, of which two launches and their dependent loads (cu,
+// lengths, pages, rows) are nearly all.  In the scalar form these take 130 and 26
+// us; it serves the other shapes.
 #include "f32x2.cuh"
 #include "paged.cuh"
 #include "quant.cuh"
@@ -713,7 +722,7 @@ void fill_geometry(const Geometry& g, int max_pages, P* p) {
   p->v_scales_head = static_cast<long long>(g.v_scales_head);
 }
 
-// Whether the vector form's conditions hold.
+// Whether the vector form's conditions hold (figures of both forms at the top).
 bool vector_form(const AppendCall& a) {
   const int D = a.g.D, g = a.g.group;
   const size_t es = a.in_dtype == KVQ_BF16 ? 2 : 4;

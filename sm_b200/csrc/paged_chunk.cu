@@ -7,12 +7,28 @@
 // floor(128 / G) tokens, fetched by one 4-D TMA copy per 64 features (feature,
 // head of the group, KV head, token).  Per block of 128 keys the packed bytes
 // come page by page, are decoded -- (code - qmax) * scale, rounded once to
-// bf16 -- into shared-memory tiles, S = Q K^T goes to tensor memory (TMEM),
-// the softmax turns S into P (bf16) in place and O += P V accumulates in TMEM.
-// At 128 rows a block costs 4 * 128 * D * 128 FLOPs for 160 (288) bytes a key
-// at D = 128: the tensor pipe bounds it, not memory.  Two row tiles are in
-// flight so that the tensor cores work on one while the other is in the
-// softmax.
+// fp16 -- into shared-memory tiles, S = Q K^T goes to tensor memory (TMEM),
+// the softmax turns S into P (fp16) in place and O += P V accumulates in TMEM.
+//
+// fp16, not bf16: rounding K to eight bits moved the scores of long contexts so
+// far that the rows were 0.8 % of their norm off; with eleven they are 0.19 %,
+// nearly all of it the output's own bf16 rounding.  Its range is the price: a
+// kernel before this one finds the largest K and V scale of each sequence and KV
+// head and turns the query rows to fp16 (powers of two below), 6 to 18 us.
+//
+// What bounds it: at 128 rows a block costs 4 * 128 * D * 128 FLOPs for 160
+// (288) bytes a key at D = 128, so the tensor pipe and not memory; 4 x 64 rows
+// of 4 heads over 16384 keys take 107 us, 640 TFLOP/s, 40 % of the measured bf16
+// rate.  The MMAs alone would take 2.6k cycles a block of two tiles.  A block
+// takes about 4.9k: V is decoded (2.0 to 2.5k), then P V of the first tile, Q K of
+// its next block and P V of the second run before V's tile is free again, while
+// the two softmaxes (3k each) and K's decode run beside that chain.  So two row
+// tiles are in flight, and a lone tile has its scores twice: the next block's are
+// there before this one's values (24 x 40 rows: 133 -> 119 us).
+//
+// The kernel's size counts as well: roles that run side by side share the
+// instruction cache, and at 130 KB of code instead of 70 everything took a
+// quarter longer.  Each step has one site; waits and segment changes are short.
 //
 // Causal rows: a column past a row's position takes no part in its maximum and
 // its p is zero.  A *value* that is not finite would still reach such a row
@@ -30,15 +46,15 @@
 //   0        producer: two lanes copy 32 keys each (codes and scales) of half a
 //            K or V block into a ring; order K(0), K(1), V(0), K(2), ...
 //   1        MMA issuer (one thread) and TMEM owner
-//   2        Q loader
+//   2        Q loader; leaves a segment's powers to the others
 //   4..7     softmax of tile 0 (a thread a row), 8..11 of tile 1
 //   12..19   decode: warp w converts 16 keys of each block, warps 12..15 from
 //            its first half-unit, 16..19 from its second
 //   3        idle
 // K tiles are double, V has one: a second V tile leaves 27 KB for the ring, and
-// the copies' latency then costs more than the wait for V's turn (a ring of 59
-// KB and one V tile: 104 us for 4 x 64 rows over 16384 keys; 27 KB and two: 107;
-// at 8 bits, prompts: 348 against 369 us).
+// the copies' latency then costs more than the wait for V's turn (in bf16, ring of
+// 59 KB and one V tile: 104 us for 4 x 64 rows over 16384 keys; 27 KB and two:
+// 107; at 8 bits, prompts: 348 against 369 us).  63 KB are no faster than 55.
 // TMEM columns: S/P of tile t at [128 t, +128), O at [256 + 128 t, +D).
 // Shared-memory tiles use the 128-byte-swizzled UMMA layout of tc_common.cuh.
 #include <cuda.h>
@@ -1053,7 +1069,8 @@ kvq_status launch(const AttendArgs& a, cudaStream_t s) {
   p.partials = reinterpret_cast<float*>(ws + l.partials);
   float* q_pow = reinterpret_cast<float*>(ws + l.powers);
   uint32_t* tops = reinterpret_cast<uint32_t*>(ws + l.tops);
-  // four CTAs an SM where the sequences and heads alone are fewer
+  // four CTAs an SM where the sequences and heads alone are fewer (two: the same
+  // within 1 us)
   const long long bh = static_cast<long long>(a.S) * a.g.H_kv;
   const int parts = static_cast<int>(std::min<long long>(kParts, std::max<long long>(1, (4 * 148 + bh - 1) / bh)));
   p.tops = tops;

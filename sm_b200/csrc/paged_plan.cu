@@ -6,7 +6,8 @@
 // independently normalized blocks"): M = max m_c, w_c = 2^(m_c - M),
 // O = sum w_c u_c / sum w_c z_c over the parts c that hold a key.  It is
 // bound by latency: the m and z of up to 32 parts come in one round (lane =
-// part), the u rows in a second whose loads do not depend on one another.
+// part), the u rows in a second whose loads do not depend on one another.  (9 us
+// with cold caches, of which the launch and the plan run beside the attention.)
 #include "paged.cuh"
 
 namespace kvq {
@@ -408,6 +409,8 @@ kvq_status launch_merge(const MergeCall& c, cudaStream_t s) {
   p.err = error_word();
   if (!p.err) return KVQ_ERR_CUDA;
   const long long heads = c.items * c.t.H;
+  // (By item throughout, 1000 sequences of 8 rows take 1709 instead of 494 us: the
+  // CTAs of items that one worker covered look up their parts for nothing.)
   p.by_item = heads <= c.workers;
   p.units = p.by_item ? static_cast<int>(heads) : c.workers - 1;
   // one more CTA reports bad sequences; with units by boundary a few look for

@@ -1,5 +1,5 @@
-// Paged attention of few query rows a KV head (decode, drafted tokens): D 64,
-// 128 or 256, groups of 32, 4- or 8-bit codes, bf16 or f32 rows.
+// Paged attention of few query rows a KV head (decode, drafted tokens): D 64
+// or 128, groups of 32, 4- or 8-bit codes, bf16 or f32 rows.
 //
 // Both contractions run on the tensor cores (mma.sync m16n8k16, bf16 in, f32
 // out) with the *codes* as the 16-row operand: integers of at most eight bits
@@ -12,13 +12,19 @@
 // for each 32-feature slice.  q' and p' are f32 values split into two bf16
 // terms (three for f32 rows) that take neighbouring columns of the 8-column
 // operand: four query rows fill a tile, and the result has the precision of
-// 16 (24) bits.
+// 16 (24) bits.  The tensor cores cut their sums off instead of rounding them:
+// f32 rows add them up outside (without that, rows over long contexts were 1.7e-6
+// of their norm off instead of 4e-7, for 0.7 us of 16).
 //
 // What bounds it: at four rows a KV head a 4-bit token costs 160 bytes, 7
-// cycles of one SM's share of the measured memory bandwidth, and about 20 warp
-// instructions, 5 cycles at full issue; half of these take the codes apart (a
+// cycles of one SM's share of the measured memory bandwidth, and about 28 warp
+// instructions, 7 cycles at full issue; half of these take the codes apart (a
 // shift and one three-input logic operation make two bf16 integers of a
-// word's nibbles 16 bits apart).  A 32-token block of one page -- codes and
+// word's nibbles 16 bits apart).  Issue is 58 % busy, the integer pipe 48 %: 32
+// x 4096 keys of 8 KV heads (168 MB) take 54.5 us, 3.1 TB/s; at 8 bits, where a
+// byte costs fewer instructions, 455 MB take 122 us, 3.7 TB/s, 56 % of the
+// measured copy rate.  Small calls (one sequence, 11 us) are two launches and the
+// latency of a few dependent loads each.  A 32-token block of one page -- codes and
 // scales -- is fetched by the warp that uses it with 16-byte asynchronous
 // copies (two blocks in flight a warp), placed so that every later
 // shared-memory read is free of bank conflicts.  A warp is a worker of the

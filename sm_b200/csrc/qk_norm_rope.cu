@@ -7,6 +7,9 @@
 // features is held by a few lanes, 16 bytes each, so one load brings a row's
 // part, shuffles give the sum of squares and (pairs D/2 apart) the partner,
 // and a warp takes several heads of one token, whose angles it loads once.
+// 172 MB (8 thousand tokens of 32 + 8 heads, D = 128) take 36 us, 4.7 TB/s, 72 %
+// of the measured copy rate; forms with fewer registers and more warps took 40 to
+// 43.  A step of 64 tokens takes 5 us, a launch.
 #include <type_traits>
 
 #include "f32x2.cuh"
