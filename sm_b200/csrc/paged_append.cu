@@ -19,8 +19,8 @@
 //
 // Bound by memory where the call is large, by latency where it is small.  8
 // thousand new tokens of 8 heads, D = 128, and reading 8 thousand back: 140 MB in
-// 69 us (2.0 TB/s; append 32, gather 27); one token of each of 64 sequences, and
-// as many read back: 17 us, of which two launches and their dependent loads (cu,
+// 68 us (2.0 TB/s); one token of each of 64 sequences, and
+// as many read back: 16 us, of which two launches and their dependent loads (cu,
 // lengths, pages, rows) are nearly all.  In the scalar form these take 130 and 26
 // us; it serves the other shapes.
 #include "f32x2.cuh"
@@ -610,36 +610,48 @@ __device__ __forceinline__ float value_at(const uint8_t* codes, long long flat, 
   return __fmul_rn(static_cast<float>(c), scale);
 }
 
-// Four consecutive codes from flat index i (a multiple of 4) less qmax.
-__device__ __forceinline__ void codes4(const uint8_t* codes, long long i, int bits, float (&c)[4]) {
+// W (8 or 4) consecutive codes from flat index i, a multiple of W, as they lie in memory.
+template <int W>
+__device__ __forceinline__ uint2 load_codes(const uint8_t* codes, long long i, int bits) {
   if (bits == 8) {
-    const unsigned w = *reinterpret_cast<const unsigned*>(codes + i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = static_cast<float>(static_cast<int>((w >> (8 * k)) & 255u) - 127);
-  } else {
-    const unsigned w = *reinterpret_cast<const unsigned short*>(codes + i / 2);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = static_cast<float>(static_cast<int>((w >> (4 * k)) & 15u) - 7);
+    if (W == 8) return __ldg(reinterpret_cast<const uint2*>(codes + i));
+    return make_uint2(__ldg(reinterpret_cast<const unsigned*>(codes + i)), 0u);
   }
+  if (W == 8) return make_uint2(__ldg(reinterpret_cast<const unsigned*>(codes + i / 2)), 0u);
+  return make_uint2(__ldg(reinterpret_cast<const unsigned short*>(codes + i / 2)), 0u);
 }
-__device__ __forceinline__ void store4(void* p, long long i, const float (&x)[4], int dtype) {
+// Code k of them, less qmax.
+__device__ __forceinline__ float code_at(const uint2& w, int k, int bits) {
+  if (bits == 8) return static_cast<float>(static_cast<int>(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 255u) - 127);
+  return static_cast<float>(static_cast<int>((w.x >> (4 * k)) & 15u) - 7);
+}
+template <int W>
+__device__ __forceinline__ void store_values(void* p, long long i, const float (&x)[W], int dtype) {
   if (dtype == KVQ_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
-        make_uint2(*reinterpret_cast<const unsigned*>(&a), *reinterpret_cast<const unsigned*>(&b));
+#pragma unroll
+    for (int k = 0; k < W; k += 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    return;
   }
+  unsigned u[W / 2];
+#pragma unroll
+  for (int k = 0; k < W; k += 2) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[k], x[k + 1]);
+    u[k / 2] = *reinterpret_cast<const unsigned*>(&a);
+  }
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p) + i;
+  if constexpr (W == 8) *reinterpret_cast<uint4*>(out) = make_uint4(u[0], u[1], u[2], u[3]);
+  else *reinterpret_cast<uint2*>(out) = make_uint2(u[0], u[1]);
 }
 
 // A CTA takes kGatherRows rows: a warp finds each row's page, then a thread
-// takes four features of one head (kVec; else one) of all the rows, so the
-// loads of the rows do not wait for one another.
-constexpr int kGatherRows = 4, kGatherThreads = 256;
-template <bool kVec>
+// takes W features (8, 4 or 1) of one head of all the rows: first every row's
+// loads, then the values and stores, so that no load waits for another's row.
+constexpr int kGatherRows = 4, kGatherThreads = 128;
+template <int W>
 __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(GatherParams p) {
   griddep_wait();
-  __shared__ int s_page[kGatherRows], s_at[kGatherRows];
+  __shared__ int s_page[kGatherRows], s_at[kGatherRows], s_group[kGatherRows];
   const long long row0 = static_cast<long long>(blockIdx.x) * kGatherRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < kGatherRows) {
@@ -665,39 +677,64 @@ __global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(GatherPara
     if (lane == 0) {
       s_page[warp] = page;
       s_at[warp] = at;
+      s_group[warp] = max(at, 0) / p.group;
     }
   }
   __syncthreads();
-  constexpr int W = kVec ? 4 : 1;
-  const int per_head = p.D / W, width = p.H * p.D;
+  const int per_head = p.D / W, width = p.H * p.D, vgs = p.Dp / p.group;
   for (int i = threadIdx.x; i < p.H * per_head; i += kGatherThreads) {
-    const int h = i / per_head, d = (i - h * per_head) * W;
+    const int h = i / per_head, d = (i - h * per_head) * W, vg = d / p.group;
+    if constexpr (W > 1) {
+      uint2 kc[kGatherRows], vc[kGatherRows];
+      float4 ks[kGatherRows][W / 4];
+      float vs[kGatherRows];
 #pragma unroll
-    for (int k = 0; k < kGatherRows; ++k) {
-      const int page = s_page[k], at = s_at[k];
-      if (page < 0) continue;
-      const long long head = static_cast<long long>(page) * p.H + h;
-      const long long o = (row0 + k) * width + h * p.D + d;
-      const long long t = max(at, 0);
-      const float* ks = p.k_scales + head * p.k_scales_head + (t / p.group) * p.D + d;
-      const float* vs = p.v_scales + head * p.v_scales_head + t * (p.Dp / p.group) + d / p.group;
-      if constexpr (kVec) {
-        float kc[4], vc[4];
-        codes4(p.k_codes + head * p.k_codes_head, t * p.D + d, p.bits, kc);
-        codes4(p.v_codes + head * p.v_codes_head, t * p.Dp + d, p.bits, vc);
-        const float4 s4 = *reinterpret_cast<const float4*>(ks);
-        const float sv = *vs;
-        float ko[4] = {__fmul_rn(kc[0], s4.x), __fmul_rn(kc[1], s4.y), __fmul_rn(kc[2], s4.z), __fmul_rn(kc[3], s4.w)};
-        float vo[4] = {__fmul_rn(vc[0], sv), __fmul_rn(vc[1], sv), __fmul_rn(vc[2], sv), __fmul_rn(vc[3], sv)};
-        if (at < 0) {
+      for (int k = 0; k < kGatherRows; ++k) {
+        const long long head = static_cast<long long>(max(s_page[k], 0)) * p.H + h, t = max(s_at[k], 0);
+        if (s_page[k] < 0) continue;
+        if (p.K) {
+          kc[k] = load_codes<W>(p.k_codes + head * p.k_codes_head, t * p.D + d, p.bits);
+          const float* at = p.k_scales + head * p.k_scales_head + static_cast<long long>(s_group[k]) * p.D + d;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ko[e] = vo[e] = 0.f;
+          for (int e = 0; e < W / 4; ++e) ks[k][e] = __ldg(reinterpret_cast<const float4*>(at) + e);
         }
-        if (p.K) store4(p.K, o, ko, p.dtype);
-        if (p.V) store4(p.V, o, vo, p.dtype);
-      } else {
-        const float kv = value_at(p.k_codes + head * p.k_codes_head, t * p.D + d, p.bits, *ks);
-        const float vv = value_at(p.v_codes + head * p.v_codes_head, t * p.Dp + d, p.bits, *vs);
+        if (p.V) {
+          vc[k] = load_codes<W>(p.v_codes + head * p.v_codes_head, t * p.Dp + d, p.bits);
+          vs[k] = __ldg(p.v_scales + head * p.v_scales_head + t * vgs + vg);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kGatherRows; ++k) {
+        if (s_page[k] < 0) continue;
+        const long long o = (row0 + k) * width + h * p.D + d;
+        const bool zero = s_at[k] < 0;
+        float x[W];
+        if (p.K) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const float4& s4 = ks[k][e / 4];
+            const float sc = (e & 3) == 0 ? s4.x : (e & 3) == 1 ? s4.y : (e & 3) == 2 ? s4.z : s4.w;
+            x[e] = zero ? 0.f : __fmul_rn(code_at(kc[k], e, p.bits), sc);
+          }
+          store_values<W>(p.K, o, x, p.dtype);
+        }
+        if (p.V) {
+#pragma unroll
+          for (int e = 0; e < W; ++e) x[e] = zero ? 0.f : __fmul_rn(code_at(vc[k], e, p.bits), vs[k]);
+          store_values<W>(p.V, o, x, p.dtype);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGatherRows; ++k) {
+        const int page = s_page[k], at = s_at[k];
+        if (page < 0) continue;
+        const long long head = static_cast<long long>(page) * p.H + h, t = max(at, 0);
+        const long long o = (row0 + k) * width + h * p.D + d;
+        const float kv = value_at(p.k_codes + head * p.k_codes_head, t * p.D + d, p.bits,
+                                  p.k_scales[head * p.k_scales_head + static_cast<long long>(s_group[k]) * p.D + d]);
+        const float vv = value_at(p.v_codes + head * p.v_codes_head, t * p.Dp + d, p.bits,
+                                  p.v_scales[head * p.v_scales_head + t * vgs + vg]);
         if (p.K) store_from_f32(p.K, o, at >= 0 ? kv : 0.f, p.dtype);
         if (p.V) store_from_f32(p.V, o, at >= 0 ? vv : 0.f, p.dtype);
       }
@@ -822,8 +859,9 @@ kvq_status launch_gather(const GatherCall& a, cudaStream_t s) {
   p.dtype = a.out_dtype;
   p.err = error_word();
   if (!p.err) return KVQ_ERR_CUDA;
-  // four features together: codes in one load, one V scale
-  auto kernel = a.g.D % 4 == 0 && a.g.group % 4 == 0 ? paged_gather_kernel<true> : paged_gather_kernel<false>;
+  // eight or four features together: codes in one load, one V scale
+  const int both = a.g.D | a.g.group;
+  auto kernel = both % 8 == 0 ? paged_gather_kernel<8> : both % 4 == 0 ? paged_gather_kernel<4> : paged_gather_kernel<1>;
   if (launch_pdl(kernel, dim3((a.T + kGatherRows - 1) / kGatherRows), dim3(kGatherThreads), 0, s, p) != cudaSuccess)
     return KVQ_ERR_CUDA;
   count_launch();
