@@ -171,10 +171,18 @@ __device__ __forceinline__ int find_item(const PlanView& v, int H, long long g) 
 struct Range {
   long long g0, g1, per, total;
 };
-__device__ __forceinline__ Range worker_range(const PlanView& v, int H, int workers, long long w) {
+// spread > 0: a worker takes at least sqrt(spread * blocks of an average (item,
+// head)) blocks, fewer workers with fewer parts to join than there could be: with
+// t a block's time and u that of joining a part, n blocks over w workers take n /
+// w t + w u, least at n / w = sqrt(n u / t).
+__device__ __forceinline__ Range worker_range(const PlanView& v, int H, int workers, long long w, float spread = 0.f) {
   Range r;
   r.total = static_cast<long long>(H) * v.pre[v.items];
   r.per = (r.total + workers - 1) / workers;
+  if (spread > 0.f && v.items > 0) {
+    const float n = static_cast<float>(v.pre[v.items]) / static_cast<float>(v.items);
+    r.per = max(r.per, static_cast<long long>(sqrtf(spread * n) + 0.5f));
+  }
   r.g0 = min(r.total, w * r.per);
   r.g1 = min(r.total, r.g0 + r.per);
   return r;
@@ -258,6 +266,7 @@ struct MergeCall {
   PlanMem plan;
   long long items;               // launch bound
   int RI, BT, workers, D;
+  float spread;                  // of worker_range
   const float* partials;
   void* O;
   int o_dtype;

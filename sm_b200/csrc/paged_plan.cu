@@ -126,7 +126,7 @@ __device__ __forceinline__ Parts find_parts(const MergeParams& p, const PlanView
   const MergeCall& c = p.c;
   const int H = c.t.H;
   Parts q{};
-  const Range r = worker_range(v, H, c.workers, 0);
+  const Range r = worker_range(v, H, c.workers, 0, c.spread);
   long long start;
   int nb;
   if (p.by_item) {

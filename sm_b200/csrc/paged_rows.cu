@@ -14,7 +14,7 @@
 // operand: four query rows fill a tile, and the result has the precision of
 // 16 (24) bits.  The tensor cores cut their sums off instead of rounding them:
 // f32 rows add them up outside (without that, rows over long contexts were 1.7e-6
-// of their norm off instead of 4e-7, for 0.7 us of 16).
+// of their norm off instead of 4e-7, for 0.7 us of 16 at the time).
 //
 // What bounds it: at four rows a KV head a 4-bit token costs 160 bytes, 7
 // cycles of one SM's share of the measured memory bandwidth, and about 28 warp
@@ -23,7 +23,7 @@
 // word's nibbles 16 bits apart).  Issue is 58 % busy, the integer pipe 48 %: 32
 // x 4096 keys of 8 KV heads (168 MB) take 54.5 us, 3.1 TB/s; at 8 bits, where a
 // byte costs fewer instructions, 455 MB take 122 us, 3.7 TB/s, 56 % of the
-// measured copy rate.  Small calls (one sequence, 11 us) are two launches and the
+// measured copy rate.  Small calls (one sequence, 10.6 us) are two launches and the
 // latency of a few dependent loads each.  A 32-token block of one page -- codes and
 // scales -- is fetched by the warp that uses it with 16-byte asynchronous
 // copies (two blocks in flight a warp), placed so that every later
@@ -35,6 +35,7 @@
 // "Block KV decoding: less workspace, more time"
 // (huhohoo.com/en/docs/llm/kv-block-decode-cost, section "Do not average
 // independently normalized blocks").
+#include <algorithm>
 #include <type_traits>
 
 #include "f32x2.cuh"
@@ -60,6 +61,7 @@ struct Params {
   void* O;
   float* partials;
   int workers;
+  float spread;
   unsigned int* err;
 };
 
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
   const int H = p.t.H, G = p.t.G, H_q = H * G, P = p.t.P;
   // neighbouring workers sit in different CTAs: a short list still uses every SM
   const long long w = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-  const Range wr = worker_range(v, H, p.workers, w);
+  const Range wr = worker_range(v, H, p.workers, w, p.spread);
   if (wr.g0 >= wr.g1) return;
 
   unsigned char* base = smem + warp * C::kWarp;
@@ -728,7 +730,15 @@ struct Run {
     p.qscale = a.scale * kLog2e;
     p.O = a.O;
     p.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan_bytes(a, C::RI));
-    p.workers = ctas(a) * C::kWarps;
+    // no more CTAs than a fourth of the blocks that the tables could hold (one
+    // sequence of 1000 keys, 8 heads: 10.8 us with 296 CTAs, 9.9 with 64)
+    const long long most = plan_items(a, C::RI) * a.g.H_kv * ((static_cast<long long>(p.t.cap) + kBT - 1) / kBT);
+    const int n = a.splits > 0 ? a.splits : static_cast<int>(std::min<long long>(ctas(a), (most + 3) / 4));
+    p.workers = n * C::kWarps;
+    // a block of 32 keys takes about 12 times as long as joining a part (one
+    // sequence of 16384 keys, 8 heads: 34 us with a worker for every two blocks, 27
+    // so); the caller's own splits are as given
+    p.spread = a.splits > 0 ? 0.f : 1.f / 12.f;
     p.err = error_word();
     if (!p.err) return KVQ_ERR_CUDA;
     if (p.plan.count) {
@@ -738,7 +748,7 @@ struct Run {
     const size_t smem = C::kWarps * C::kWarp + (p.plan.count ? 0 : (a.S + 1) * sizeof(int));
     auto kernel = paged_rows_kernel<BITS, D, NT, NS>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
-    if (launch_pdl(kernel, dim3(ctas(a)), dim3(32 * C::kWarps), smem, s, p) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (launch_pdl(kernel, dim3(n), dim3(32 * C::kWarps), smem, s, p) != cudaSuccess) return KVQ_ERR_CUDA;
     count_launch();
     MergeCall m{};
     m.t = p.t;
@@ -747,6 +757,7 @@ struct Run {
     m.RI = C::RI;
     m.BT = kBT;
     m.workers = p.workers;
+    m.spread = p.spread;
     m.D = D;
     m.partials = p.partials;
     m.O = a.O;
