@@ -19,8 +19,8 @@
 //
 // Bound by memory where the call is large, by latency where it is small.  8
 // thousand new tokens of 8 heads, D = 128, and reading 8 thousand back: 140 MB in
-// 68 us (2.0 TB/s); one token of each of 64 sequences, and
-// as many read back: 16 us, of which two launches and their dependent loads (cu,
+// 63 us (2.2 TB/s); one token of each of 64 sequences, and
+// as many read back: 15.5 us, of which two launches and their dependent loads (cu,
 // lengths, pages, rows) are nearly all.  In the scalar form these take 130 and 26
 // us; it serves the other shapes.
 #include "f32x2.cuh"
@@ -647,9 +647,11 @@ __device__ __forceinline__ void store_values(void* p, long long i, const float (
 // A CTA takes kGatherRows rows: a warp finds each row's page, then a thread
 // takes W features (8, 4 or 1) of one head of all the rows: first every row's
 // loads, then the values and stores, so that no load waits for another's row.
-constexpr int kGatherRows = 4, kGatherThreads = 128;
+// (Append and read-back of 8 thousand tokens: 68 us with four rows, 63 with two, 65
+// with one.)
+constexpr int kGatherRows = 2, kGatherThreads = 128;
 template <int W>
-__global__ void __launch_bounds__(kGatherThreads) paged_gather_kernel(GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads, 8) paged_gather_kernel(GatherParams p) {
   griddep_wait();
   __shared__ int s_page[kGatherRows], s_at[kGatherRows], s_group[kGatherRows];
   const long long row0 = static_cast<long long>(blockIdx.x) * kGatherRows;
