@@ -13,8 +13,9 @@
 // fp16, not bf16: rounding K to eight bits moved the scores of long contexts so
 // far that the rows were 0.8 % of their norm off; with eleven they are 0.19 %,
 // nearly all of it the output's own bf16 rounding.  Its range is the price: a
-// kernel before this one finds the largest K and V scale of each sequence and KV
-// head and turns the query rows to fp16 (powers of two below), 6 to 18 us.
+// kernel before this one finds the largest and the smallest K and V scale of each
+// sequence and KV head and turns the query rows to fp16 (powers of two below), 6
+// to 18 us.
 //
 // What bounds it: at 128 rows a block costs 4 * 128 * D * 128 FLOPs for 160
 // (288) bytes a key at D = 128, so the tensor pipe and not memory; 4 x 64 rows
@@ -47,10 +48,10 @@
 //            K or V block into a ring; order K(0), K(1), V(0), K(2), ...
 //   1        MMA issuer (one thread) and TMEM owner
 //   2        Q loader; leaves a segment's powers to the others
+//   3        finds the CTA's form, which says what bodies 4..19 run
 //   4..7     softmax of tile 0 (a thread a row), 8..11 of tile 1
 //   12..19   decode: warp w converts 16 keys of each block, warps 12..15 from
 //            its first half-unit, 16..19 from its second
-//   3        idle
 // K tiles are double, V has one: a second V tile leaves 27 KB for the ring, and
 // the copies' latency then costs more than the wait for V's turn (in bf16, ring of
 // 59 KB and one V tile: 104 us for 4 x 64 rows over 16384 keys; 27 KB and two:
@@ -80,19 +81,41 @@ constexpr float kLazy = 8.f;
 constexpr int kTileHalf = kBT * 128;              // 16 KB: 128 rows x 64 bf16
 constexpr int kMaxUnits = 12;                    // half-units of the ring
 
-// Powers of two that keep the fp16 tiles in range.  The tiles hold (code - qmax)
-// * scale * 2^(kTop - e), below 2^15 (the scale is below 2^(e + 1), the code at
-// most 2^7 away from zero), where e is the exponent of the largest K (V) scale of
-// the sequence and KV head; a query row is multiplied by 2^(kTopQ - e) of its own.
-// Nothing but the powers changes with what is far away or behind a row's position:
-// the bits do not, short of values 2^21 below the largest scale, where fp16 loses
-// precision.
+// Powers of two that keep the fp16 tiles in range.  A query row is multiplied by
+// 2^(kTopQ - e) of its own, e the exponent of its largest element.  For K and V
+// there are two forms, chosen for a segment by its sequence's and KV head's scales:
+//
+//   narrow  the largest K (V) scale is at most 2^kSpread times the smallest: the
+//           tiles hold (code - qmax) * scale * 2^(kTop - e), e the exponent of the
+//           largest.  That is below 2^15 (the scale is below 2^(e + 1), the code
+//           at most 2^7 away from zero), and a code of one times the smallest scale
+//           is a normal fp16 number, so nothing but the power depends on it.
+//   wide    a key's row of K (of V) is multiplied by 2^(kTopQ - e_t) of its own
+//           largest value, as query rows are.  The decode warps leave the powers in
+//           shared memory; a column's score is multiplied by K's, and V's exponent
+//           joins the weight: with w_t = (s_t - m) + e_t (log2 units, m the score's
+//           reference), p'_t = 2^(w_t - R) for a row's own lazy reference R of w
+//           (it follows m), z sums p_t = 2^(s_t - m) as always, and O = sum p'_t
+//           (v_t 2^(kTopQ - e_t)) 2^(R - kTopQ) / z.
+//           So a key that a row does not see changes nothing of the row's, a group
+//           of zeros (whose scale is 1) is a group of zeros, and what is lost is
+//           what float32 sums lose too: contributions below 2^-21 of the largest.
+//           Its softmax waits for V's tile: more time, for data that is rarely met.
 constexpr int kTop = 7, kTopQ = 14;
 constexpr float kTopP = 7.f;                     // p <= 2^(kTopP + kLazy) = 2^15
 constexpr int kExpMin = -100, kExpMax = 127;
-constexpr int kParts = 16;                       // of a sequence's groups, at most, each with a maximum of its own
+constexpr int kSpread = 21;                      // 2^kTop * 2^-kSpread = 2^-14, the smallest normal fp16 number
+constexpr int kWide = 1 << 10;                   // in place of an exponent: the segment's form is wide
+constexpr int kParts = 16;                       // of a sequence's groups, at most, each with extremes of its own
+constexpr uint32_t kInfBits = 0x7f800000u;
 
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// Whether scales from `least` to `most` (bits; most 0: none that is finite) are too
+// far apart for the narrow form.
+__device__ __forceinline__ bool spread_wide(uint32_t most, uint32_t least) {
+  return most > 0u && (static_cast<int>(most >> 23) - static_cast<int>(least >> 23) > kSpread ||
+                       static_cast<int>(least >> 23) - 127 < kExpMin - kSpread);
+}
 // exponent of a value given by its bits
 __device__ __forceinline__ int exponent(uint32_t bits) {
   return min(max(static_cast<int>(bits >> 23) - 127, kExpMin), kExpMax);
@@ -107,9 +130,12 @@ struct Smem {
   static constexpr int kRing = kV + kTile;
   static constexpr int kRingBytes = 55 * 1024;
   static constexpr int kBar = kRing + kRingBytes;
-  static constexpr int kMisc = kBar + 58 * 8;      // TMEM base, abort flag, non-finite tokens [8] (64-bit)
-  static constexpr int kPow = kMisc + 80;          // int2 [4]: a segment's exponents (K, V)
-  static constexpr int kPre = kPow + 32;            // int pre[S + 1] (inline plan)
+  static constexpr int kMisc = kBar + 58 * 8;      // TMEM base, abort flag, the CTA's form
+  static constexpr int kBad = kMisc + 16;          // uint64 [8]: a segment's non-finite tokens
+  static constexpr int kPow = kBad + 8 * 8;        // int2 [4]: a segment's exponents (K, V), or kWide
+  static constexpr int kKeyPow = kPow + 32;         // float [4][kBT]: powers of the keys of four K tiles (wide form)
+  static constexpr int kValExp = kKeyPow + 4 * kBT * 4;   // float [kBT]: exponents of V's rows (wide form)
+  static constexpr int kPre = kValExp + kBT * 4;    // int pre[S + 1] (inline plan)
 };
 
 enum Bar {
@@ -125,6 +151,7 @@ enum Bar {
   Q_READY = 51,
   Q_FREE = 52,
   POWERS = 53,                   // [4]
+  FORM = 57,                     // the CTA's form is known
 };
 
 struct Params {
@@ -134,7 +161,7 @@ struct Params {
   const float* k_scales;
   const uint8_t* v_codes;
   const float* v_scales;
-  const uint32_t* tops;          // [S][H][2][kParts]: bits of the largest K and V scales
+  const uint32_t* tops;          // [S][H][4][kParts]: bits of the largest K and V scales, kInfBits less the smallest's
   int parts;                     // of them in use
   const float* q_pow;            // [T][H_q]: 2^(e - kTopQ) of a query row
   float qscale;                  // scale * log2(e)
@@ -196,16 +223,18 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------------------
-// decode of a unit's 16 keys to bf16 values in a swizzled tile
+// decode of a unit's 16 keys to fp16 values in a swizzled tile
 // ---------------------------------------------------------------------------
 // A lane takes 16 features (two 16-byte chunks of the tile) of a token; at D =
 // 128 a quarter warp is one token, and lanes q and q + 4 store their chunks in
 // opposite order, so the quarter warp meets eight bank groups; at D = 64 it is
 // two tokens, whose rows swizzle differently.
-template <int BITS, int D, bool kV>
+// kWideForm: the values' power is the key's own and goes to s_key[t]: K's inverse
+// power, V's exponent.
+template <int BITS, int D, bool kV, bool kWideForm>
 __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned char* dst, int wk, int lane, int nv,
                                             float power, int t_base, unsigned long long seg_key,
-                                            unsigned long long* s_bad) {
+                                            unsigned long long* s_bad, float* s_key) {
   constexpr int kCb = D * BITS / 8, QN = D / 16, TPP = 32 / QN;
   const int q = lane % QN, tt = lane / QN;
   const bool swap = D == 128 && (q & 4) != 0;
@@ -224,8 +253,10 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
         ks[4 * i + 2] = pack2(v1.x, v1.y);
         ks[4 * i + 3] = pack2(v1.z, v1.w);
       }
+      if (!kWideForm) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ks[i] = mul2(ks[i], pack2(power, power));
+        for (int i = 0; i < 8; ++i) ks[i] = mul2(ks[i], pack2(power, power));
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) ks[i] = 0ull;
@@ -236,6 +267,11 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
   for (int it = 0; it < 16 / TPP; ++it) {
     const int t = 16 * wk + TPP * it + tt, tu = 16 * w4 + TPP * it + tt;
     uint4 o[2];
+    u64 own[8];                                    // wide form: the values, then times the key's power
+    if (kWideForm) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) own[i] = 0ull;
+    }
     if (t < nv) {
       u64 s2 = 0ull;
       if (kV) {
@@ -244,7 +280,7 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
           atomicMax(s_bad, seg_key | static_cast<unsigned>(0x7fffffff - (t_base + t)));
           s = 0.f;
         }
-        s *= power;
+        if (!kWideForm) s *= power;
         s2 = pack2(s, s);
       }
       uint32_t h[8];
@@ -257,7 +293,8 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
           for (int r = 0; r < 4; ++r) {
             const u64 f = fma2(nibble_pair(byte_at15(w[i], r)), mul, add);
             const u64 x = mul2(f, kV ? s2 : ks[4 * i + r]);
-            h[4 * i + r] = pack_f16(lo_f(x), hi_f(x));
+            if (kWideForm) own[4 * i + r] = x;
+            else h[4 * i + r] = pack_f16(lo_f(x), hi_f(x));
           }
       } else {
         const uint4 w4 = *reinterpret_cast<const uint4*>(u + tu * kCb + 16 * q);
@@ -268,14 +305,33 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
           for (int r = 0; r < 4; r += 2) {
             const u64 f = add2(byte_pair(w[i], r), sub);
             const u64 x = mul2(f, kV ? s2 : ks[2 * i + r / 2]);
-            h[2 * i + r / 2] = pack_f16(lo_f(x), hi_f(x));
+            if (kWideForm) own[2 * i + r / 2] = x;
+            else h[2 * i + r / 2] = pack_f16(lo_f(x), hi_f(x));
           }
       }
-      o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-      o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+      if (!kWideForm) {
+        o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+      }
     } else {
       o[0] = make_uint4(0u, 0u, 0u, 0u);
       o[1] = o[0];
+    }
+    if (kWideForm) {
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        m = max(m, max(static_cast<uint32_t>(own[i]) & 0x7fffffffu, static_cast<uint32_t>(own[i] >> 32) & 0x7fffffffu));
+#pragma unroll
+      for (int x = 1; x < QN; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+      const int e = exponent(m);
+      const float f = exp2i(kTopQ - e);
+      uint32_t h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = pack_f16(lo_f(own[i]) * f, hi_f(own[i]) * f);
+      o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+      if (q == 0) s_key[t] = kV ? static_cast<float>(e) : exp2i(e - kTopQ);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -321,9 +377,95 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
   }
 }
 
+// A block's softmax in the wide form, for a warp's rows: the references and z
+// move, O (D columns at o_col) is rescaled where they do, and P replaces S at s_col.
+// nv: columns the row sees; s_key, s_val: the block's powers and exponents.  O may be
+// rescaled once pv_bar's phase is over (0: it is).
+struct WideRow {
+  float m, z, r;                  // the score's reference; sum of the weights; the reference of weight + exponent
+};
+template <int D>
+__device__ __forceinline__ WideRow softmax_wide(WideRow w, uint32_t s_col, uint32_t o_col, float qs, int nv,
+                                             const float* s_key, const float* s_val, uint32_t v_bar, uint32_t v_parity,
+                                             bool first, uint32_t pv_bar, uint32_t pv_parity,
+                                             volatile int* abort_flag) {
+  const int seen = __reduce_max_sync(0xffffffffu, nv);
+  // scores of 16 columns, each less `less`
+  auto scores = [&](float (&x)[16], int cc, float less) {
+    uint32_t sr[16];
+    KVQ_LD16(sr, s_col + 16u * cc);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __fmul_rn(__uint_as_float(sr[e]), qs * s_key[16 * cc + e]) - less;
+  };
+  float x[16];
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int cc = 0; 16 * cc < seen; ++cc) {
+    scores(x, cc, 0.f);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (16 * cc + e < nv) top = fmaxf(top, x[e]);
+  }
+  if (top > w.m + kLazy) {
+    w.z *= ex2(w.m - top);                               // 0 where the row had no key
+    w.r += w.m - top;
+    w.m = top;
+  }
+  // V's exponents come with its tile.  (The phase before this one is over: this
+  // row's tile waited for it, or, where a segment begins, the MMA issuer did before
+  // the scores.)
+  wait(v_bar, v_parity, abort_flag);
+  top = -INFINITY;
+#pragma unroll 1
+  for (int cc = 0; 16 * cc < seen; ++cc) {
+    scores(x, cc, w.m);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (16 * cc + e < nv) top = fmaxf(top, x[e] + s_val[16 * cc + e]);
+  }
+  const bool need = top > w.r + kLazy;
+  if (__any_sync(0xffffffffu, need)) {
+    const float a = need ? ex2(w.r - top) : 1.f;
+    if (need) w.r = top;
+    if (!first) {
+      if (pv_bar) {
+        wait(pv_bar, pv_parity, abort_flag);
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int oc = 0; oc < D / 16; ++oc) {
+        uint32_t orr[16];
+        KVQ_LD16(orr, o_col + 16u * oc);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+        KVQ_ST16(o_col + 16u * oc, orr);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int cc = 0; cc < 8; ++cc) {
+    const int left = nv - 16 * cc;
+    uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (16 * cc < seen) {
+      scores(x, cc, w.m);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (e < left) w.z += ex2(x[e] + kTopP);
+        x[e] = e < left ? ex2(x[e] + (s_val[16 * cc + e] - w.r) + kTopP) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pk[e] = pack_f16(x[2 * e], x[2 * e + 1]);
+    }
+    KVQ_ST8(s_col + 8u * cc, pk);
+  }
+  return w;
+}
+
 // What the attention needs beforehand.  The first S * H * parts CTAs find the
-// largest K and V scales of a sequence and KV head, in parts of its groups of 32
-// tokens, a warp a group: they read the scales alone (32 of 160 bytes a token at D
+// largest and smallest K and V scales of a sequence and KV head, in parts of its
+// groups of 32 tokens, a warp a group: they read the scales alone (32 of 160 bytes a token at D
 // = 128 and 4 bits), and the attention finds them in the L2 afterwards.  The
 // others turn the query rows to fp16, D / 8 lanes a row.  (Turned in shared memory
 // by the softmax, at a segment's start, prompts took 419 us instead of 397.)
@@ -374,7 +516,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   const int b = bh / t.H, h = bh % t.H;
   const SeqView s = seq_view(t, b);
   const int32_t* table = t.table + static_cast<long long>(b) * t.max_pages;
-  uint32_t top[2] = {0u, 0u};
+  uint32_t top[4] = {0u, 0u, 0u, 0u};                     // K's and V's largest, kInfBits less the smallest
   // lane i looks up the page of the warp's i-th group, 32 at a time; then the
   // scales of four groups are on their way together
   const int stride = parts * kPrepareWarps, groups = s.n > 0 ? (s.len + 31) >> 5 : 0;
@@ -399,30 +541,367 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
       for (int i = 0; i < 4; ++i) {
         const bool live = 32 * (g0 + min(i0 + i, n - 1) * stride) + lane < s.len;   // the lane's token
 #pragma unroll
-        for (int e = 0; e < 2 * D / 32; ++e) {            // (what is not finite stays that whatever the power)
+        for (int e = 0; e < 2 * D / 32; ++e) {            // (zero, and what is not finite, stays that whatever the power)
           const uint32_t v = reinterpret_cast<const uint32_t*>(&x[i][e / (D / 32)])[e % (D / 32)] & 0x7fffffffu;
-          if (v < 0x7f800000u && (e < D / 32 || live)) top[e / (D / 32)] = max(top[e / (D / 32)], v);
+          if (v - 1u < kInfBits - 1u && (e < D / 32 || live)) {
+            top[e / (D / 32)] = max(top[e / (D / 32)], v);
+            top[2 + e / (D / 32)] = max(top[2 + e / (D / 32)], kInfBits - v);
+          }
         }
       }
     }
   }
-  __shared__ uint32_t s_top[2][kPrepareWarps];
+  __shared__ uint32_t s_top[4][kPrepareWarps];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, top[i]);
     if (lane == 0) s_top[i][warp] = m;
   }
   __syncthreads();
-  if (threadIdx.x < 2) {
+  if (threadIdx.x < 4) {
     uint32_t m = 0u;
     for (int w = 0; w < kPrepareWarps; ++w) m = max(m, s_top[threadIdx.x][w]);
-    tops[(static_cast<long long>(bh) * 2 + threadIdx.x) * kParts + part] = m;
+    tops[(static_cast<long long>(bh) * 4 + threadIdx.x) * kParts + part] = m;
   }
   if (beside) griddep_join();
 }
 
+// ---------------------------------------------------------------------------
+// the decode and softmax roles
+// ---------------------------------------------------------------------------
+// What they need of their CTA.
 template <int BITS, int D>
-__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ CUtensorMap qmap, Params p) {
+struct Cta {
+  using M = Smem<D>;
+  static constexpr int kCodes = D * BITS / 8;             // code bytes of a key
+  static constexpr int kScales = D * 8;                   // scale bytes of a half-unit (K: 2 groups x D; V: 64 x D / 32)
+  static constexpr int kUnit = kBT / 2 * kCodes + kScales;
+  static constexpr uint32_t kUnits = M::kRingBytes / kUnit < kMaxUnits ? M::kRingBytes / kUnit : kMaxUnits;
+  const Params& p;
+  Walk walk;
+  Range wr;
+  unsigned char* sm;
+  uint32_t base, tmem;
+  __device__ __forceinline__ uint32_t bar(int i) const { return base + M::kBar + 8u * static_cast<uint32_t>(i); }
+};
+
+// kWideToo: a segment may have the wide form.
+template <int BITS, int D, bool kWideToo>
+__device__ __forceinline__ void decode_role(const Cta<BITS, D>& cta) {
+  using M = Smem<D>;
+  const Params& p = cta.p;
+  const Walk& walk = cta.walk;
+  const Range& wr = cta.wr;
+  unsigned char* const sm = cta.sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return cta.bar(i); };
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + M::kMisc + 4);
+  unsigned long long* const s_bad = reinterpret_cast<unsigned long long*>(sm + M::kBad);
+  const int2* const s_pow = reinterpret_cast<const int2*>(sm + M::kPow);
+  float* const s_key = reinterpret_cast<float*>(sm + M::kKeyPow);
+  float* const s_val = reinterpret_cast<float*>(sm + M::kValExp);
+  constexpr uint32_t nu = Cta<BITS, D>::kUnits;
+  constexpr int unit_bytes = Cta<BITS, D>::kUnit;
+  const int wk = warp - 12;
+  const int half = wk >> 2;
+  uint32_t slot = half, wraps = 0, kb = 0, seg = 0;    // kb: K blocks decoded; V's are one behind
+  Place c = walk.begin(wr);
+  int t0 = 0, nv = 0;                                 // V's block
+  bool start = false;
+  uint32_t segs = 0;                                  // segments begun
+  int2 pw = make_int2(0, 0);                          // K's and V's block's
+  int ev = 0;
+  auto arrived = [&]() {
+    wait(bar(RING_FULL + 2 * slot + half), wraps >> (nu & 1u) & 1u, abort_flag);
+    return sm + M::kRing + slot * unit_bytes;
+  };
+  auto finished = [&](uint32_t ready) {
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(ready);
+      mbar_arrive(bar(RING_EMPTY + slot));
+    }
+    slot += 2;
+    if (slot >= nu) {
+      slot -= nu;
+      ++wraps;
+    }
+  };
+#pragma unroll 1
+  for (;; ++kb) {                                     // K(kb), then V(kb - 1)
+    const int t0_k = c.j * kBT, nv_k = c.s.len - t0_k;
+    const bool more = c.left > 0, start_k = c.start;
+    if (more) {
+      const uint32_t buf = kb & 1u;
+      if (start_k) {
+        wait(bar(POWERS + (segs & 3u)), segs >> 2 & 1u, abort_flag);
+        pw = s_pow[segs & 3u];
+        ++segs;
+      }
+      const unsigned char* u = arrived();
+      if (kb >= 2) wait(bar(K_FREE + buf), ((kb >> 1) - 1) & 1u, abort_flag);
+      // (a key's powers are read by the softmax, after the tile's buffer is free
+      // again: four of them)
+      if (kWideToo && pw.x == kWide)
+        decode_unit<BITS, D, false, true>(u, sm + M::kK + buf * M::kTile, wk, lane, min(kBT, nv_k), 0.f, 0, 0, nullptr,
+                                         s_key + (kb & 3u) * kBT);
+      else
+        decode_unit<BITS, D, false, false>(u, sm + M::kK + buf * M::kTile, wk, lane, min(kBT, nv_k),
+                                           exp2i(kTop - pw.x), 0, 0, nullptr, nullptr);
+      finished(bar(K_READY + buf));
+      walk.next(c);
+    }
+    if (kb > 0) {
+      const uint32_t v = kb - 1;
+      const unsigned char* u = arrived();
+      if (v >= 1) wait(bar(V_FREE), (v - 1) & 1u, abort_flag);
+      if (start) ++seg;
+      const unsigned long long key = static_cast<unsigned long long>(seg) << 32;
+      if (kWideToo && ev == kWide)
+        decode_unit<BITS, D, true, true>(u, sm + M::kV, wk, lane, min(kBT, nv), 0.f, t0, key, s_bad + (seg & 7u), s_val);
+      else
+        decode_unit<BITS, D, true, false>(u, sm + M::kV, wk, lane, min(kBT, nv), exp2i(kTop - ev), t0, key,
+                                          s_bad + (seg & 7u), nullptr);
+      finished(bar(V_READY));
+    }
+    if (!more) break;
+    t0 = t0_k;
+    nv = nv_k;
+    start = start_k;
+    ev = pw.y;
+  }
+}
+
+// One query row a thread.
+template <int BITS, int D, bool kWideToo>
+__device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
+  using M = Smem<D>;
+  const Params& p = cta.p;
+  const Walk& walk = cta.walk;
+  const Range& wr = cta.wr;
+  unsigned char* const sm = cta.sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return cta.bar(i); };
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + M::kMisc + 4);
+  unsigned long long* const s_bad = reinterpret_cast<unsigned long long*>(sm + M::kBad);
+  const int2* const s_pow = reinterpret_cast<const int2*>(sm + M::kPow);
+  float* const s_key = reinterpret_cast<float*>(sm + M::kKeyPow);
+  float* const s_val = reinterpret_cast<float*>(sm + M::kValExp);
+  const int H = p.t.H, G = p.t.G, TR = p.TT * G;
+  const uint32_t tmem = cta.tmem;
+  const int tile = (warp - 4) >> 2;
+  const int r = ((warp & 3) << 5) + lane;            // TMEM lane = row within the tile
+  const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t o_col = tmem + lane_addr + 256u + 128u * tile;
+  const bool neg = p.qscale < 0.f;
+  float m_ref = -INFINITY, z = 0.f;
+  float qs = 0.f, ov = 0.f;                           // what the row's scores and its O are multiplied by;
+                                                      // wide form: ov is R, the reference of weight + exponent
+  uint32_t k[2] = {0, 0}, seg = 0;                    // blocks of the tile's S and of its other one (tile 1: and
+                                                      // those it has no part in); segments of the CTA
+  bool other = true;
+  long long row = 0;                                  // of Q and O
+  int lim = 0;                                        // keys the row sees
+  bool real = false;                                  // the row exists
+  bool first_seg = true, seg_is_first = true, from_zero = false;
+#pragma unroll 1
+  for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
+    if (c.start) {
+      ++seg;
+      seg_is_first = first_seg;
+      first_seg = false;
+      from_zero = c.j == 0;
+      const int rr = c.it.r0 + tile * TR + r;
+      real = r < TR && rr < c.s.n * G;
+      lim = real ? row_limit(p.t, c.s, rr) : c.s.len;  // rows that do not exist take the unmasked path
+      row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
+      m_ref = -INFINITY;
+      z = 0.f;
+      qs = real ? __ldcg(p.q_pow + row) : 0.f;        // (no row: equal scores, never a new reference)
+    }
+    const bool lone = walk.tiles(c) == 1;
+    if (lone && tile) {
+      if (kWideToo) ++k[1];
+      continue;
+    }
+    other = lone && !c.start && !other;               // a lone tile takes its two in turn
+    const int u = other ? 2 : tile;
+    const uint32_t s_col = tmem + lane_addr + (u > 0 ? 128u : 0u), nth = other ? k[1] : k[0];
+    wait(bar(S_FULL + u), nth & 1u, abort_flag);
+    const int2 pw = s_pow[(seg - 1) & 3u];            // (written before the query rows were asked for)
+    const bool wide = kWideToo && pw.x == kWide;
+    if (c.start) {
+      qs = p.qscale * qs * (wide ? 1.f : exp2i(pw.x - kTop));
+      ov = wide ? -INFINITY : exp2i(pw.y - kTop);
+    }
+    tc_fence_after();
+    const int nv = min(kBT, lim - c.j * kBT);       // columns the row sees
+    if (wide) {
+      const uint32_t blk = k[0] + k[1];               // blocks of the CTA before this one
+      const WideRow w = softmax_wide<D>(WideRow{m_ref, z, ov}, s_col, o_col, qs, nv, s_key + (blk & 3u) * kBT, s_val,
+                                        bar(V_READY), blk & 1u, c.start, lone ? bar(PV_DONE + 2 - u) : 0u,
+                                        ((other ? k[0] : k[1]) - 1) & 1u, abort_flag);
+      m_ref = w.m;
+      z = w.z;
+      ov = w.r;
+    } else {
+      const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
+      const int seen = plain ? kBT : __reduce_max_sync(0xffffffffu, nv);   // columns that a row of the warp sees
+      // the row's largest score over the columns it sees (none: never a new reference)
+      float mb = -INFINITY;
+      if (plain) {
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t sr[64];
+          KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
+          KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
+          tmem_wait_ld();
+          mb = fmaxf(mb, row_max(sr));
+        }
+        mb *= qs;
+      } else {
+#pragma unroll 1
+        for (int cc = 0; 16 * cc < seen; ++cc) {
+          uint32_t sr[16];
+          KVQ_LD16(sr, s_col + 16u * cc);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (16 * cc + e < nv) mb = fmaxf(mb, __uint_as_float(sr[e]) * qs);
+        }
+      }
+      const bool need = mb > m_ref + kLazy;
+      if (__any_sync(0xffffffffu, need)) {
+        const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
+        if (need) m_ref = mb;
+        z *= a;
+        if (!c.start) {
+          if (lone) {                                   // (its S did not wait for the last product)
+            wait(bar(PV_DONE + 2 - u), ((other ? k[0] : k[1]) - 1) & 1u, abort_flag);
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int oc = 0; oc < D / 16; ++oc) {
+            uint32_t orr[16];
+            KVQ_LD16(orr, o_col + 16u * oc);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
+            KVQ_ST16(o_col + 16u * oc, orr);
+          }
+        }
+      }
+      // p = exp2(s * qs - m_ref + kTopP) as fp16 over the columns already read,
+      // 16 at a time, the next ones on their way
+      const float m_top = kTopP - m_ref;
+      u64 z2 = 0ull;
+      if (plain) {
+        uint32_t s0[16], s1[16];
+        const u64 f2 = pack2(qs, qs), c2 = pack2(m_top, m_top);
+        auto columns = [&](const uint32_t (&sr)[16], int cc) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, c2);
+            const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
+            z2 = add2(z2, pack2(p0, p1));
+            pk[e] = pack_f16(p0, p1);
+          }
+          KVQ_ST8(s_col + 8u * cc, pk);
+        };
+        KVQ_LD16(s0, s_col);
+#pragma unroll 1
+        for (int cc = 0; cc < 8; cc += 2) {
+          tmem_wait_ld();
+          KVQ_LD16(s1, s_col + 16u * cc + 16u);
+          columns(s0, cc);
+          tmem_wait_ld();
+          if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
+          columns(s1, cc + 1);
+        }
+      } else {
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {
+          const int left = nv - 16 * cc;
+          uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          if (16 * cc < seen) {
+            uint32_t sr[16];
+            KVQ_LD16(sr, s_col + 16u * cc);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = e < left ? ex2(fmaf(__uint_as_float(sr[e]), qs, m_top)) : 0.f;
+              const float p1 = e + 1 < left ? ex2(fmaf(__uint_as_float(sr[e + 1]), qs, m_top)) : 0.f;
+              z2 = add2(z2, pack2(p0, p1));
+              pk[e >> 1] = pack_f16(p0, p1);
+            }
+          }
+          KVQ_ST8(s_col + 8u * cc, pk);
+        }
+      }
+      z += lo_f(z2) + hi_f(z2);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(P_FULL + u));
+    if (other) ++k[1]; else ++k[0];
+    if (walk.last(c)) {
+      // the segment's last P V product must be done before O is read
+      wait(bar(PV_DONE + u), nth & 1u, abort_flag);
+      tc_fence_after();
+      const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
+      const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
+      const bool whole = from_zero && c.j + 1 == c.nb;
+      if (wide) ov = z == 0.f ? 0.f : ex2(ov - static_cast<float>(kTopQ));
+      const int pr = tile * 128 + r;
+      float* part = p.partials + (2 * static_cast<long long>(blockIdx.x) + (seg_is_first ? 0 : 1)) * 256 * (D + 2) +
+                    static_cast<long long>(pr >> 5) * (D + 2) * 32 + (pr & 31);
+      if (!whole) {
+        part[0] = m_ref;
+        part[32] = z;
+      }
+      // z = 0: a row without a key
+      const float inv = poison ? __uint_as_float(0x7fc00000u) : (z == 0.f ? 0.f : ov / z);
+      const float keep = poison ? inv : ov;
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t orr[32];
+        KVQ_LD32(orr, o_col + 32u * cc);
+        tmem_wait_ld();
+        if (whole) {
+          uint32_t ob[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            ob[e] = pack_bf16(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+          if (real) {
+            uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + 32 * cc);
+#pragma unroll
+            for (int qq = 0; qq < 4; ++qq)
+              dst[qq] = make_uint4(ob[4 * qq], ob[4 * qq + 1], ob[4 * qq + 2], ob[4 * qq + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[(2 + 32 * cc + e) * 32] = __uint_as_float(orr[e]) * keep;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+}
+// Both, for a CTA with such segments.  Out of line: side by side in the narrow
+// form's loops these steps cost it 4 % (drafts 119 -> 125, prompts 379 -> 395 us);
+// so, 2 % less to 2 % more (116.8, 383; 4 x 64 rows 109 -> 111.5).
+template <int BITS, int D>
+__device__ __noinline__ void wide_roles(Cta<BITS, D> cta) {
+  if (threadIdx.x >= 12 * 32) decode_role<BITS, D, true>(cta);
+  else softmax_role<BITS, D, true>(cta);
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                  const __grid_constant__ Params p) {
   using M = Smem<D>;
   griddep_wait();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -432,16 +911,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   int* s_pre = reinterpret_cast<int*>(sm + M::kPre);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + M::kMisc + 4);
   int2* s_pow = reinterpret_cast<int2*>(sm + M::kPow);
-  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + M::kMisc + 8);
+  unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + M::kBad);
   const uint32_t bar0 = base + M::kBar;
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int H = p.t.H, G = p.t.G, TR = p.TT * G;
-  constexpr int cb = D * BITS / 8;
-  constexpr int kScales = D * 8;                          // scale bytes of a half-unit (K: 2 groups x D; V: 64 x D / 32)
-  constexpr int unit_bytes = kBT / 2 * cb + kScales;
-  constexpr uint32_t nu = M::kRingBytes / unit_bytes < kMaxUnits ? M::kRingBytes / unit_bytes : kMaxUnits;
+  constexpr int cb = Cta<BITS, D>::kCodes, kScales = Cta<BITS, D>::kScales, unit_bytes = Cta<BITS, D>::kUnit;
+  constexpr uint32_t nu = Cta<BITS, D>::kUnits;
 
   if (!p.plan.count && warp == 0) warp_prefix(p.t, p.RI, kBT, s_pre);
   if (threadIdx.x == 32) {
@@ -462,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
       mbar_init(bar(PV_DONE + i), 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(POWERS + i), 1);
+    mbar_init(bar(FORM), 1);
     mbar_init(bar(V_READY), kDecodeWarps);
     mbar_init(bar(V_FREE), 1);
     mbar_init(bar(Q_READY), 1);
@@ -695,11 +1173,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
 #pragma unroll 1
       for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
         if (!c.start) continue;
-        const uint32_t x = __ldcg(p.tops + (static_cast<long long>(c.it.b) * H + c.h) * (2 * kParts) + lane);
-        const uint32_t ke = __reduce_max_sync(0xffffffffu, lane < p.parts ? x : 0u);
-        const uint32_t ve = __reduce_max_sync(0xffffffffu, lane >= kParts && lane < kParts + p.parts ? x : 0u);
+        const uint32_t* tops = p.tops + (static_cast<long long>(c.it.b) * H + c.h) * (4 * kParts) + lane;
+        const bool live = lane % kParts < p.parts;
+        const uint32_t x = live ? __ldcg(tops) : 0u, y = live ? __ldcg(tops + 2 * kParts) : 0u;
+        const uint32_t ke = __reduce_max_sync(0xffffffffu, lane < kParts ? x : 0u);
+        const uint32_t ve = __reduce_max_sync(0xffffffffu, lane < kParts ? 0u : x);
+        const uint32_t kl = kInfBits - __reduce_max_sync(0xffffffffu, lane < kParts ? y : 0u);
+        const uint32_t vl = kInfBits - __reduce_max_sync(0xffffffffu, lane < kParts ? 0u : y);
         if (lane == 0) {
-          s_pow[s & 3u] = make_int2(exponent(ke), exponent(ve));
+          s_pow[s & 3u] = spread_wide(ke, kl) || spread_wide(ve, vl) ? make_int2(kWide, kWide)
+                                                                     : make_int2(exponent(ke), exponent(ve));
           mbar_arrive(bar(POWERS + (s & 3u)));
         }
         if (s > 0) wait(bar(Q_FREE), (s - 1) & 1u, abort_flag);
@@ -717,251 +1200,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         }
       }
       if (*abort_flag && lane == 0 && s > 0) drain(bar(Q_READY), (s - 1) & 1u);
-    } else if (warp >= 12) {
-      // ======================= decode =======================
-      const int wk = warp - 12;
-      const int half = wk >> 2;
-      uint32_t slot = half, wraps = 0, kb = 0, seg = 0;    // kb: K blocks decoded; V's are one behind
-      Place c = walk.begin(wr);
-      int t0 = 0, nv = 0;                                 // V's block
-      bool start = false;
-      uint32_t segs = 0;                                  // segments begun
-      int2 pw = make_int2(0, 0);                          // K's and V's block's
-      int ev = 0;
-      auto arrived = [&]() {
-        wait(bar(RING_FULL + 2 * slot + half), wraps >> (nu & 1u) & 1u, abort_flag);
-        return sm + M::kRing + slot * unit_bytes;
-      };
-      auto finished = [&](uint32_t ready) {
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(ready);
-          mbar_arrive(bar(RING_EMPTY + slot));
-        }
-        slot += 2;
-        if (slot >= nu) {
-          slot -= nu;
-          ++wraps;
-        }
-      };
+    } else if (warp == 3) {
+      // ======================= the CTA's form =======================
+      // The largest and smallest scales over its sequences (of any head) say whether
+      // a segment can be wide: only then do the decode and softmax warps run the
+      // bodies that know that form.
+      const int b0 = plan_item(walk.v, find_item(walk.v, H, wr.g0)).b,
+                b1 = plan_item(walk.v, find_item(walk.v, H, wr.g1 - 1)).b;
+      const uint32_t* tops = p.tops + static_cast<long long>(b0) * H * (4 * kParts);
+      uint32_t most = 0u, least = 0u;                     // of lanes below kParts K's, of the others V's
+      const int n = lane % kParts < p.parts ? (b1 - b0 + 1) * H : 0;
 #pragma unroll 1
-      for (;; ++kb) {                                     // K(kb), then V(kb - 1)
-        const int t0_k = c.j * kBT, nv_k = c.s.len - t0_k;
-        const bool more = c.left > 0, start_k = c.start;
-        if (more) {
-          const uint32_t buf = kb & 1u;
-          if (start_k) {
-            wait(bar(POWERS + (segs & 3u)), segs >> 2 & 1u, abort_flag);
-            pw = s_pow[segs & 3u];
-            ++segs;
-          }
-          const unsigned char* u = arrived();
-          if (kb >= 2) wait(bar(K_FREE + buf), ((kb >> 1) - 1) & 1u, abort_flag);
-          decode_unit<BITS, D, false>(u, sm + M::kK + buf * M::kTile, wk, lane, min(kBT, nv_k),
-                                      exp2i(kTop - pw.x), 0, 0, nullptr);
-          finished(bar(K_READY + buf));
-          walk.next(c);
+      for (int i = 0; i < n; i += 8) {                    // (past the last one: the last one again)
+        uint32_t x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t* at = tops + min(i + e, n - 1) * (4 * kParts) + lane;
+          x[e] = __ldcg(at);
+          y[e] = __ldcg(at + 2 * kParts);
         }
-        if (kb > 0) {
-          const uint32_t v = kb - 1;
-          const unsigned char* u = arrived();
-          if (v >= 1) wait(bar(V_FREE), (v - 1) & 1u, abort_flag);
-          if (start) ++seg;
-          decode_unit<BITS, D, true>(u, sm + M::kV, wk, lane, min(kBT, nv), exp2i(kTop - ev), t0,
-                                     static_cast<unsigned long long>(seg) << 32, s_bad + (seg & 7u));
-          finished(bar(V_READY));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          most = max(most, x[e]);
+          least = max(least, y[e]);
         }
-        if (!more) break;
-        t0 = t0_k;
-        nv = nv_k;
-        start = start_k;
-        ev = pw.y;
+      }
+      __syncwarp();
+      bool wide = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool mine = lane / kParts == i;
+        wide |= spread_wide(__reduce_max_sync(0xffffffffu, mine ? most : 0u),
+                            kInfBits - __reduce_max_sync(0xffffffffu, mine ? least : 0u));
+      }
+      if (lane == 0) {
+        *reinterpret_cast<volatile int*>(sm + M::kMisc + 8) = wide;
+        mbar_arrive(bar(FORM));
       }
     } else if (warp >= 4) {
-      // ======================= softmax: one query row per thread =======================
-      const int tile = (warp - 4) >> 2;
-      const int r = ((warp & 3) << 5) + lane;            // TMEM lane = row within the tile
-      const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t o_col = tmem + lane_addr + 256u + 128u * tile;
-      const bool neg = p.qscale < 0.f;
-      float m_ref = -INFINITY, z = 0.f;
-      float qs = 0.f, ov = 0.f;                           // what the row's scores and its O are multiplied by
-      uint32_t k[2] = {0, 0}, seg = 0;                    // blocks of the tile's S and of its other one; segments of the CTA
-      bool other = true;
-      long long row = 0;                                  // of Q and O
-      int lim = 0;                                        // keys the row sees
-      bool real = false;                                  // the row exists
-      bool first_seg = true, seg_is_first = true, from_zero = false;
-#pragma unroll 1
-      for (Place c = walk.begin(wr); c.left > 0; walk.next(c)) {
-        if (c.start) {
-          ++seg;
-          seg_is_first = first_seg;
-          first_seg = false;
-          from_zero = c.j == 0;
-          const int rr = c.it.r0 + tile * TR + r;
-          real = r < TR && rr < c.s.n * G;
-          lim = real ? row_limit(p.t, c.s, rr) : c.s.len;  // rows that do not exist take the unmasked path
-          row = static_cast<long long>(c.s.q0 + rr / G) * (H * G) + c.h * G + rr % G;
-          m_ref = -INFINITY;
-          z = 0.f;
-          qs = real ? __ldcg(p.q_pow + row) : 0.f;        // (no row: equal scores, never a new reference)
-        }
-        const bool lone = walk.tiles(c) == 1;
-        if (lone && tile) continue;
-        other = lone && !c.start && !other;               // a lone tile takes its two in turn
-        const int u = other ? 2 : tile;
-        const uint32_t s_col = tmem + lane_addr + (u > 0 ? 128u : 0u), nth = other ? k[1] : k[0];
-        wait(bar(S_FULL + u), nth & 1u, abort_flag);
-        if (c.start) {                                    // (written before the query rows were asked for)
-          const int2 pw = s_pow[(seg - 1) & 3u];
-          qs = p.qscale * qs * exp2i(pw.x - kTop);
-          ov = exp2i(pw.y - kTop);
-        }
-        tc_fence_after();
-        const int nv = min(kBT, lim - c.j * kBT);       // columns the row sees
-        const bool plain = !neg && __all_sync(0xffffffffu, nv >= kBT);
-        const int seen = plain ? kBT : __reduce_max_sync(0xffffffffu, nv);   // columns that a row of the warp sees
-        // the row's largest score over the columns it sees (none: never a new reference)
-        float mb = -INFINITY;
-        if (plain) {
-#pragma unroll 1
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t sr[64];
-            KVQ_LD32_AT(sr, 0, s_col + 64u * hh);
-            KVQ_LD32_AT(sr, 32, s_col + 64u * hh + 32u);
-            tmem_wait_ld();
-            mb = fmaxf(mb, row_max(sr));
-          }
-          mb *= qs;
-        } else {
-#pragma unroll 1
-          for (int cc = 0; 16 * cc < seen; ++cc) {
-            uint32_t sr[16];
-            KVQ_LD16(sr, s_col + 16u * cc);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (16 * cc + e < nv) mb = fmaxf(mb, __uint_as_float(sr[e]) * qs);
-          }
-        }
-        const bool need = mb > m_ref + kLazy;
-        if (__any_sync(0xffffffffu, need)) {
-          const float a = need ? ex2(m_ref - mb) : 1.f;    // 0 where the row had no key
-          if (need) m_ref = mb;
-          z *= a;
-          if (!c.start) {
-            if (lone) {                                   // (its S did not wait for the last product)
-              wait(bar(PV_DONE + 2 - u), ((other ? k[0] : k[1]) - 1) & 1u, abort_flag);
-              tc_fence_after();
-            }
-#pragma unroll 1
-            for (int oc = 0; oc < D / 16; ++oc) {
-              uint32_t orr[16];
-              KVQ_LD16(orr, o_col + 16u * oc);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * a);
-              KVQ_ST16(o_col + 16u * oc, orr);
-            }
-          }
-        }
-        // p = exp2(s * qs - m_ref + kTopP) as fp16 over the columns already read,
-        // 16 at a time, the next ones on their way
-        const float m_top = kTopP - m_ref;
-        u64 z2 = 0ull;
-        if (plain) {
-          uint32_t s0[16], s1[16];
-          const u64 f2 = pack2(qs, qs), c2 = pack2(m_top, m_top);
-          auto columns = [&](const uint32_t (&sr)[16], int cc) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const u64 x = fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, c2);
-              const float p0 = ex2(lo_f(x)), p1 = ex2(hi_f(x));
-              z2 = add2(z2, pack2(p0, p1));
-              pk[e] = pack_f16(p0, p1);
-            }
-            KVQ_ST8(s_col + 8u * cc, pk);
-          };
-          KVQ_LD16(s0, s_col);
-#pragma unroll 1
-          for (int cc = 0; cc < 8; cc += 2) {
-            tmem_wait_ld();
-            KVQ_LD16(s1, s_col + 16u * cc + 16u);
-            columns(s0, cc);
-            tmem_wait_ld();
-            if (cc < 6) KVQ_LD16(s0, s_col + 16u * cc + 32u);
-            columns(s1, cc + 1);
-          }
-        } else {
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            const int left = nv - 16 * cc;
-            uint32_t pk[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            if (16 * cc < seen) {
-              uint32_t sr[16];
-              KVQ_LD16(sr, s_col + 16u * cc);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float p0 = e < left ? ex2(fmaf(__uint_as_float(sr[e]), qs, m_top)) : 0.f;
-                const float p1 = e + 1 < left ? ex2(fmaf(__uint_as_float(sr[e + 1]), qs, m_top)) : 0.f;
-                z2 = add2(z2, pack2(p0, p1));
-                pk[e >> 1] = pack_f16(p0, p1);
-              }
-            }
-            KVQ_ST8(s_col + 8u * cc, pk);
-          }
-        }
-        z += lo_f(z2) + hi_f(z2);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P_FULL + u));
-        if (other) ++k[1]; else ++k[0];
-        if (walk.last(c)) {
-          // the segment's last P V product must be done before O is read
-          wait(bar(PV_DONE + u), nth & 1u, abort_flag);
-          tc_fence_after();
-          const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
-          const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
-          const bool whole = from_zero && c.j + 1 == c.nb;
-          const int pr = tile * 128 + r;
-          float* part = p.partials + (2 * static_cast<long long>(blockIdx.x) + (seg_is_first ? 0 : 1)) * 256 * (D + 2) +
-                        static_cast<long long>(pr >> 5) * (D + 2) * 32 + (pr & 31);
-          if (!whole) {
-            part[0] = m_ref;
-            part[32] = z;
-          }
-          // z = 0: a row without a key
-          const float inv = poison ? __uint_as_float(0x7fc00000u) : (z == 0.f ? 0.f : ov / z);
-          const float keep = poison ? inv : ov;
-#pragma unroll 1
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t orr[32];
-            KVQ_LD32(orr, o_col + 32u * cc);
-            tmem_wait_ld();
-            if (whole) {
-              uint32_t ob[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                ob[e] = pack_bf16(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
-              if (real) {
-                uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + 32 * cc);
-#pragma unroll
-                for (int qq = 0; qq < 4; ++qq)
-                  dst[qq] = make_uint4(ob[4 * qq], ob[4 * qq + 1], ob[4 * qq + 2], ob[4 * qq + 3]);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) part[(2 + 32 * cc + e) * 32] = __uint_as_float(orr[e]) * keep;
-            }
-          }
-          tc_fence_before();
-        }
-      }
+      const Cta<BITS, D> cta{p, walk, wr, sm, base, tmem};
+      wait(bar(FORM), 0u, abort_flag);
+      const bool wide = *reinterpret_cast<volatile int*>(sm + M::kMisc + 8) != 0;
+      if (wide) wide_roles<BITS, D>(cta);
+      else if (warp >= 12) decode_role<BITS, D, false>(cta);
+      else softmax_role<BITS, D, false>(cta);
     }
   }
   tc_fence_before();
@@ -1000,7 +1282,7 @@ bool applies(const AttendArgs& a) {
 size_t partials_bytes(const AttendArgs& a) {
   return 2 * static_cast<size_t>(ctas(a)) * 256 * (a.g.D + 2) * sizeof(float);
 }
-// workspace: the plan, partial results, fp16 query rows and their powers, largest scales
+// workspace: the plan, partial results, fp16 query rows and their powers, largest and smallest scales
 struct Layout {
   size_t partials, rows, powers, tops, bytes;
 };
@@ -1012,7 +1294,7 @@ Layout layout(const AttendArgs& a) {
   l.rows = l.partials + up(partials_bytes(a));
   l.powers = l.rows + up(rows * a.g.D * 2);
   l.tops = l.powers + up(rows * sizeof(float));
-  l.bytes = l.tops + 2 * sizeof(uint32_t) * kParts * a.S * a.g.H_kv;
+  l.bytes = l.tops + 4 * sizeof(uint32_t) * kParts * a.S * a.g.H_kv;
   return l;
 }
 size_t workspace(const AttendArgs& a) { return layout(a).bytes; }
