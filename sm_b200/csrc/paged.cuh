@@ -88,10 +88,16 @@ struct Item {
   int r0;       // first row within the sequence's n * G rows
 };
 
+// (64 bits: f32 rows have an item a few rows, and 2^17 of these over 2^19 keys are
+// 2^31 blocks, a matter of seconds.)
 struct PlanView {
-  const int* pre;       // [items + 1] prefix of block counts (one head)
+  const long long* pre; // [items + 1] prefix of block counts (one head)
   const Item* item;     // nullptr: item i is sequence i, row 0
   int items;
+  // blocks of item i (below 2^26: the low words' difference)
+  __device__ __forceinline__ int blocks(int i) const {
+    return static_cast<int>(static_cast<unsigned>(pre[i + 1]) - static_cast<unsigned>(pre[i]));
+  }
 };
 
 struct AttendArgs {
@@ -210,34 +216,34 @@ inline size_t align16(size_t n) { return (n + 15) / 16 * 16; }
 inline size_t plan_bytes(const AttendArgs& a, int RI) {
   if (plan_inline(a, RI)) return 0;
   const size_t n = static_cast<size_t>(plan_items(a, RI));
-  return align16(16 + (n + 1) * sizeof(int)) + align16(n * sizeof(Item));
+  return align16(16 + (n + 1) * sizeof(long long)) + align16(n * sizeof(Item));
 }
 struct PlanMem {
   int* count;           // nullptr: in-kernel prefix
-  int* pre;
+  long long* pre;
   Item* item;
 };
 inline PlanMem plan_mem(const AttendArgs& a, int RI, void* ws) {
   if (plan_inline(a, RI)) return PlanMem{nullptr, nullptr, nullptr};
   char* p = static_cast<char*>(ws);
   const size_t n = static_cast<size_t>(plan_items(a, RI));
-  return PlanMem{reinterpret_cast<int*>(p), reinterpret_cast<int*>(p + 16),
-                 reinterpret_cast<Item*>(p + align16(16 + (n + 1) * sizeof(int)))};
+  return PlanMem{reinterpret_cast<int*>(p), reinterpret_cast<long long*>(p + 16),
+                 reinterpret_cast<Item*>(p + align16(16 + (n + 1) * sizeof(long long)))};
 }
 kvq_status launch_plan(const AttendArgs& a, const PlanMem& m, int RI, int BT, cudaStream_t s);
 
 // One warp: the block prefix over the sequences, into pre[0..S] (shared
 // memory; the caller synchronises).
-__device__ __forceinline__ void warp_prefix(const Batch& t, int RI, int BT, int* pre) {
+__device__ __forceinline__ void warp_prefix(const Batch& t, int RI, int BT, long long* pre) {
   const int lane = threadIdx.x & 31;
-  int carry = 0;
+  long long carry = 0;
   for (int base = 0; base < t.S; base += 32) {
     const int b = base + lane;
-    int v = 0;
+    long long v = 0;
     if (b < t.S) v = item_blocks(t, seq_view(t, b), 0, RI, BT);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, v, o);
+      const long long n = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += n;
     }
     if (b < t.S) pre[b + 1] = carry + v;
@@ -247,7 +253,7 @@ __device__ __forceinline__ void warp_prefix(const Batch& t, int RI, int BT, int*
 }
 
 // The view a kernel uses: the workspace's plan, or the CTA's own prefix.
-__device__ __forceinline__ PlanView plan_view(const PlanMem& m, const int* s_pre, int S) {
+__device__ __forceinline__ PlanView plan_view(const PlanMem& m, const long long* s_pre, int S) {
   if (m.count) return PlanView{m.pre, m.item, *m.count};
   return PlanView{s_pre, nullptr, S};
 }

@@ -135,7 +135,7 @@ struct Smem {
   static constexpr int kPow = kBad + 8 * 8;        // int2 [4]: a segment's exponents (K, V), or kWide
   static constexpr int kKeyPow = kPow + 32;         // float [4][kBT]: powers of the keys of four K tiles (wide form)
   static constexpr int kValExp = kKeyPow + 4 * kBT * 4;   // float [kBT]: exponents of V's rows (wide form)
-  static constexpr int kPre = kValExp + kBT * 4;    // int pre[S + 1] (inline plan)
+  static constexpr int kPre = kValExp + kBT * 4;    // int64 pre[S + 1] (inline plan)
 };
 
 enum Bar {
@@ -176,7 +176,7 @@ struct Params {
 // ---------------------------------------------------------------------------
 struct Place {
   int i, h, j, nb;
-  long long left;
+  int left;                      // blocks from here to the CTA's end (2^31 would take it an hour)
   Item it;
   SeqView s;
   bool start;                    // first block of a segment
@@ -187,11 +187,11 @@ struct Walk {
   __device__ __forceinline__ void enter(Place& a) const {
     a.it = plan_item(v, a.i);
     a.s = seq_view(p.t, a.it.b);
-    a.nb = v.pre[a.i + 1] - v.pre[a.i];
+    a.nb = v.blocks(a.i);
   }
   __device__ __forceinline__ Place begin(const Range& r) const {
     Place a;
-    a.left = r.g1 - r.g0;
+    a.left = static_cast<int>(r.g1 - r.g0);
     a.start = true;
     if (a.left <= 0) return a;
     a.i = find_item(v, p.t.H, r.g0);
@@ -210,7 +210,7 @@ struct Walk {
     if (++a.h == p.t.H) {
       a.h = 0;
       do ++a.i;
-      while (v.pre[a.i + 1] == v.pre[a.i]);
+      while (v.blocks(a.i) == 0);
       enter(a);
     }
   }
@@ -891,8 +891,7 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
   }
 }
 // Both, for a CTA with such segments.  Out of line: side by side in the narrow
-// form's loops these steps cost it 4 % (drafts 119 -> 125, prompts 379 -> 395 us);
-// so, 2 % less to 2 % more (116.8, 383; 4 x 64 rows 109 -> 111.5).
+// form's loops these steps cost it 4 % (drafts 119 -> 125, prompts 379 -> 395 us).
 template <int BITS, int D>
 __device__ __noinline__ void wide_roles(Cta<BITS, D> cta) {
   if (threadIdx.x >= 12 * 32) decode_role<BITS, D, true>(cta);
@@ -908,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   const uint32_t raw_addr = su(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   unsigned char* sm = smem_raw + (base - raw_addr);
-  int* s_pre = reinterpret_cast<int*>(sm + M::kPre);
+  long long* s_pre = reinterpret_cast<long long*>(sm + M::kPre);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + M::kMisc + 4);
   int2* s_pow = reinterpret_cast<int2*>(sm + M::kPow);
   unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + M::kBad);
@@ -1266,7 +1265,7 @@ int item_rows(const AttendArgs& a) {
 }
 template <int D>
 size_t smem_bytes(const AttendArgs& a) {
-  return 1024 + Smem<D>::kPre + (plan_inline(a, item_rows(a)) ? sizeof(int) * (a.S + 1) : 0);
+  return 1024 + Smem<D>::kPre + (plan_inline(a, item_rows(a)) ? sizeof(long long) * (a.S + 1) : 0);
 }
 size_t smem_of(const AttendArgs& a) { return a.g.D == 64 ? smem_bytes<64>(a) : smem_bytes<128>(a); }
 

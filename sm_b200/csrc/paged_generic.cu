@@ -44,7 +44,7 @@ __device__ __forceinline__ int code_at(const uint8_t* codes, long long flat, int
 
 size_t smem_bytes(int D, int S) {
   return (static_cast<size_t>(2 * kBT * (D + 1) + 2 * kRT * D + kRT * kBT + 3 * kRT) + kRT) * sizeof(float) +
-         static_cast<size_t>(kBT + S + 1) * sizeof(int);
+         kBT * sizeof(int) + (static_cast<size_t>(S) + 1) * sizeof(long long);
 }
 
 __global__ void __launch_bounds__(kThreads) paged_generic_kernel(Params p) {
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(Params p) {
   float* s_a = s_z + kRT;
   int* s_lim = reinterpret_cast<int*>(s_a + kRT);     // [kRT] keys each row sees
   int* s_page = s_lim + kRT;                          // [kBT] page of each token of the block
-  int* s_pre = s_page + kBT;                          // [S + 1]
+  long long* s_pre = reinterpret_cast<long long*>(s_page + kBT);   // [S + 1] (an even number of words comes before)
 
   if (!p.plan.count && threadIdx.x < 32) warp_prefix(p.t, kRT, kBT, s_pre);
   __syncthreads();
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(Params p) {
   if (wr.g0 >= wr.g1) return;
 
   int i = find_item(v, H, wr.g0);
-  int nb = v.pre[i + 1] - v.pre[i];
+  int nb = v.blocks(i);
   const long long off = wr.g0 - static_cast<long long>(H) * v.pre[i];
   int h = static_cast<int>(off / nb), j = static_cast<int>(off % nb);
   long long g = wr.g0;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) paged_generic_kernel(Params p) {
       h = 0;
       do {
         ++i;
-        nb = v.pre[i + 1] - v.pre[i];
+        nb = v.blocks(i);
       } while (nb == 0);
     }
   }

@@ -16,44 +16,46 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// Sum of two counts, held below 2^30: a cu that is not as stated can give
-// the sequences more rows than there are, and the prefix must stay ordered.
-__device__ __forceinline__ int add_sat(int a, int b) { return min(a + b, 0x3fffffff); }
+// Sum of two counts of items, held below 2^30: a cu that is not as stated can
+// give the sequences more rows than there are, and the prefix must stay ordered.
+__device__ __forceinline__ int add(int a, int b) { return min(a + b, 0x3fffffff); }
+// Of blocks: at most 2^30 items of 2^26 each.
+__device__ __forceinline__ long long add(long long a, long long b) { return a + b; }
 
 // Inclusive scan of one count per thread over the CTA.
-__device__ __forceinline__ int block_scan(int v, int* s_warp) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* s_warp) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v = add_sat(v, n);
+    const T n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v = add(v, n);
   }
   if (lane == 31) s_warp[w] = v;
   __syncthreads();
   if (w == 0) {
-    int x = s_warp[lane];
+    T x = s_warp[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x = add_sat(x, n);
+      const T n = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = add(x, n);
     }
     s_warp[lane] = x;
   }
   __syncthreads();
-  const int add = w > 0 ? s_warp[w - 1] : 0;
+  const T before = w > 0 ? s_warp[w - 1] : T(0);
   __syncthreads();
-  return add_sat(v, add);
+  return add(v, before);
 }
 
-// One CTA.  Item counts of the sequences are summed into s_first (sequences
-// 1024 at a time, the prefix kept in the workspace's pre array until the
-// items' own prefix replaces it: pre has room for items + 1 >= the sequences
-// that have rows, so the sequences' prefix lives in shared memory instead).
+// One CTA.  Item counts of the sequences are summed into s_first (shared memory,
+// sequences 1024 at a time), then the items' block counts into the plan.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch t, PlanMem m, int RI, int BT, int max_items,
                                                             unsigned int* err) {
   griddep_wait();
   extern __shared__ int s_first[];              // [S + 1] first item of each sequence
   __shared__ int s_warp[32];
+  __shared__ long long s_warp_blocks[32];
   int carry = 0;
   for (int base = 0; base < t.S; base += kPlanThreads) {
     const int b = base + static_cast<int>(threadIdx.x);
@@ -64,17 +66,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch t, PlanMem m, 
       v = (s.n * t.G + RI - 1) / RI;
     }
     const int inc = block_scan(v, s_warp);
-    if (b < t.S) s_first[b + 1] = add_sat(carry, inc);
+    if (b < t.S) s_first[b + 1] = add(carry, inc);
     __syncthreads();
     carry = s_first[min(base + kPlanThreads, t.S)];
   }
   if (threadIdx.x == 0) s_first[0] = 0;
   __syncthreads();
   const int items = min(s_first[t.S], max_items);
-  int blocks = 0;
+  long long blocks = 0;
   for (int base = 0; base < items; base += kPlanThreads) {
     const int i = base + static_cast<int>(threadIdx.x);
-    int v = 0;
+    long long v = 0;
     if (i < items) {
       int lo = 0, hi = t.S - 1;                 // largest b with s_first[b] <= i
       while (lo < hi) {
@@ -86,11 +88,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Batch t, PlanMem m, 
       v = item_blocks(t, seq_view(t, lo), r0, RI, BT);
       m.item[i] = Item{lo, r0};
     }
-    const int inc = block_scan(v, s_warp);
-    if (i < items) m.pre[i + 1] = add_sat(blocks, inc);
-    if (threadIdx.x == kPlanThreads - 1) s_warp[0] = inc;
+    const long long inc = block_scan(v, s_warp_blocks);
+    if (i < items) m.pre[i + 1] = add(blocks, inc);
+    if (threadIdx.x == kPlanThreads - 1) s_warp_blocks[0] = inc;
     __syncthreads();
-    blocks = add_sat(blocks, s_warp[0]);
+    blocks = add(blocks, s_warp_blocks[0]);
     __syncthreads();
   }
   if (threadIdx.x == 0) {
@@ -133,14 +135,14 @@ __device__ __forceinline__ Parts find_parts(const MergeParams& p, const PlanView
     q.i = unit / H;
     q.h = unit % H;
     if (q.i >= v.items) return q;
-    nb = v.pre[q.i + 1] - v.pre[q.i];
+    nb = v.blocks(q.i);
     start = static_cast<long long>(H) * v.pre[q.i] + static_cast<long long>(q.h) * nb;
     q.mine = true;
   } else {
     const long long x = (unit + 1) * r.per;
     if (x >= r.total) return q;
     q.i = find_item(v, H, x);
-    nb = v.pre[q.i + 1] - v.pre[q.i];
+    nb = v.blocks(q.i);
     q.h = static_cast<int>((x - static_cast<long long>(H) * v.pre[q.i]) / nb);
     start = static_cast<long long>(H) * v.pre[q.i] + static_cast<long long>(q.h) * nb;
     q.mine = x > start && x - r.per <= start;
@@ -180,7 +182,8 @@ __device__ __forceinline__ float exp2_w(float x) {
 // once per CTA) and the wait for the attention kernel.  The inline plan reads
 // only the call's inputs (through the L2), so it runs while that kernel
 // drains; the workspace's plan is read after the wait.
-__device__ __forceinline__ PlanView merge_prologue(const MergeParams& p, int unit, int* s_pre, Parts* s_parts) {
+__device__ __forceinline__ PlanView merge_prologue(const MergeParams& p, int unit, long long* s_pre,
+                                                   Parts* s_parts) {
   const bool global = p.c.plan.count != nullptr;
   if (global) griddep_wait();
   if (threadIdx.x < 32) {
@@ -205,7 +208,7 @@ __device__ __forceinline__ void odd_jobs(const MergeParams& p, const PlanView& v
       if (seq_view(c.t, b).bad) record_error(p.err, KVQ_ERR_LENGTH);
   if (p.by_item) return;
   for (int i = z; i < v.items; i += nz) {
-    if (v.pre[i + 1] != v.pre[i]) continue;
+    if (v.blocks(i) != 0) continue;
     Parts q{};
     q.it = plan_item(v, i);
     q.s = seq_view(c.t, q.it.b);
@@ -225,7 +228,7 @@ __device__ __forceinline__ void odd_jobs(const MergeParams& p, const PlanView& v
 constexpr int kMergeWarps = 4;
 template <bool kVec>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(MergeParams p) {
-  extern __shared__ int s_pre[];
+  extern __shared__ long long s_pre[];
   __shared__ Parts s_parts;
   __shared__ float s_u[kMergeWarps][256];
   const MergeCall& c = p.c;
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_rows_kernel(MergeParam
 // as often: five prompts took 397 instead of 385 us.)
 template <int D>
 __global__ void __launch_bounds__(256) merge_tiles_kernel(MergeParams p) {
-  extern __shared__ int s_pre[];
+  extern __shared__ long long s_pre[];
   __shared__ Parts s_parts;
   const MergeCall& c = p.c;
   const PlanView v = merge_prologue(p, blockIdx.x, s_pre, &s_parts);
@@ -416,7 +419,7 @@ kvq_status launch_merge(const MergeCall& c, cudaStream_t s) {
   // one more CTA reports bad sequences; with units by boundary a few look for
   // items without a key
   const unsigned gx = static_cast<unsigned>(p.units) + (p.by_item ? 1 : 16);
-  const size_t smem = c.plan.count ? 0 : (static_cast<size_t>(c.t.S) + 1) * sizeof(int);
+  const size_t smem = c.plan.count ? 0 : (static_cast<size_t>(c.t.S) + 1) * sizeof(long long);
   cudaError_t e;
   if (c.tile_rows > 0) {
     auto kernel = c.D == 64 ? merge_tiles_kernel<64> : merge_tiles_kernel<128>;

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
   using C = Cfg<BITS, D, NT, NS>;
   griddep_wait();
   extern __shared__ __align__(128) unsigned char smem[];
-  int* s_pre = reinterpret_cast<int*>(smem + C::kWarps * C::kWarp);
+  long long* s_pre = reinterpret_cast<long long*>(smem + C::kWarps * C::kWarp);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   if (!p.plan.count) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
   auto enter = [&](Place& a) {                 // the item of place a
     a.it = plan_item(v, a.i);
     a.s = seq_view(p.t, a.it.b);
-    a.nb = v.pre[a.i + 1] - v.pre[a.i];
+    a.nb = v.blocks(a.i);
   };
   auto advance = [&](Place& a) {               // the next block; true where a new segment begins
     if (--a.left == 0) return false;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
     if (++a.h == H) {
       a.h = 0;
       do ++a.i;
-      while (v.pre[a.i + 1] == v.pre[a.i]);
+      while (v.blocks(a.i) == 0);
       enter(a);
     }
     return true;
@@ -745,7 +745,7 @@ struct Run {
       const kvq_status st = launch_plan(a, p.plan, C::RI, kBT, s);
       if (st != KVQ_OK) return st;
     }
-    const size_t smem = C::kWarps * C::kWarp + (p.plan.count ? 0 : (a.S + 1) * sizeof(int));
+    const size_t smem = C::kWarps * C::kWarp + (p.plan.count ? 0 : (a.S + 1) * sizeof(long long));
     auto kernel = paged_rows_kernel<BITS, D, NT, NS>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return KVQ_ERR_CUDA;
     if (launch_pdl(kernel, dim3(n), dim3(32 * C::kWarps), smem, s, p) != cudaSuccess) return KVQ_ERR_CUDA;
