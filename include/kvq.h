@@ -399,7 +399,10 @@ KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t*
  *   splits   as kvq_attend.
  * A row without a visible key is zero.  Sums, the softmax's maximum and sum
  * and the weighted values are float32; O is rounded once.  What lies behind a
- * row's position may hold anything, infinities and NaN included.
+ * row's position may hold anything, infinities and NaN included.  A V scale that
+ * is not finite makes a row that sees its token not finite in that scale's g
+ * features; a K scale that is not finite makes the whole row so, unless its
+ * scores are all minus infinity.
  * Calls of many bf16 rows (kvq_paged_kernel_name says "paged_chunk_tcgen05")
  * round K, V and the softmax's weights once to fp16, in ranges that keep eleven
  * bits of each: a key's values lose precision only where they are 2^28 times

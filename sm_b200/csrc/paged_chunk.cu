@@ -33,8 +33,9 @@
 //
 // Causal rows: a column past a row's position takes no part in its maximum and
 // its p is zero.  A *value* that is not finite would still reach such a row
-// through 0 * inf, so its token's scale is taken as zero in the tile and the
-// token is remembered: rows that do see it become NaN at the segment's end.
+// through 0 * inf, so its scale is taken as zero in the tile and the token is
+// remembered with the scale's 32 features: there, rows that do see it become NaN at
+// the segment's end.
 //
 // The softmax reads S twice (its maximum, then p): a read of 32 columns takes
 // about 70 cycles, a vote and a branch per 32 columns in a single pass took four
@@ -131,8 +132,8 @@ struct Smem {
   static constexpr int kRingBytes = 55 * 1024;
   static constexpr int kBar = kRing + kRingBytes;
   static constexpr int kMisc = kBar + 58 * 8;      // TMEM base, abort flag, the CTA's form
-  static constexpr int kBad = kMisc + 16;          // uint64 [8]: a segment's non-finite tokens
-  static constexpr int kPow = kBad + 8 * 8;        // int2 [4]: a segment's exponents (K, V), or kWide
+  static constexpr int kBad = kMisc + 16;          // uint64 [8][4]: a segment's non-finite tokens, per 32 features
+  static constexpr int kPow = kBad + 8 * 4 * 8;    // int2 [4]: a segment's exponents (K, V), or kWide
   static constexpr int kKeyPow = kPow + 32;         // float [4][kBT]: powers of the keys of four K tiles (wide form)
   static constexpr int kValExp = kKeyPow + 4 * kBT * 4;   // float [kBT]: exponents of V's rows (wide form)
   static constexpr int kPre = kValExp + kBT * 4;    // int64 pre[S + 1] (inline plan)
@@ -276,8 +277,8 @@ __device__ __forceinline__ void decode_unit(const unsigned char* u, unsigned cha
       u64 s2 = 0ull;
       if (kV) {
         float s = sc[D / 32 * tu + (q >> 1)];
-        if (!(fabsf(s) < INFINITY)) {              // remembered: rows that see the token become NaN
-          atomicMax(s_bad, seg_key | static_cast<unsigned>(0x7fffffff - (t_base + t)));
+        if (!(fabsf(s) < INFINITY)) {              // remembered: rows that see the token become NaN there
+          atomicMax(s_bad + (q >> 1), seg_key | static_cast<unsigned>(0x7fffffff - (t_base + t)));
           s = 0.f;
         }
         if (!kWideForm) s *= power;
@@ -659,10 +660,10 @@ __device__ __forceinline__ void decode_role(const Cta<BITS, D>& cta) {
       if (start) ++seg;
       const unsigned long long key = static_cast<unsigned long long>(seg) << 32;
       if (kWideToo && ev == kWide)
-        decode_unit<BITS, D, true, true>(u, sm + M::kV, wk, lane, min(kBT, nv), 0.f, t0, key, s_bad + (seg & 7u), s_val);
+        decode_unit<BITS, D, true, true>(u, sm + M::kV, wk, lane, min(kBT, nv), 0.f, t0, key, s_bad + 4 * (seg & 7u), s_val);
       else
         decode_unit<BITS, D, true, false>(u, sm + M::kV, wk, lane, min(kBT, nv), exp2i(kTop - ev), t0, key,
-                                          s_bad + (seg & 7u), nullptr);
+                                          s_bad + 4 * (seg & 7u), nullptr);
       finished(bar(V_READY));
     }
     if (!more) break;
@@ -851,8 +852,6 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
       // the segment's last P V product must be done before O is read
       wait(bar(PV_DONE + u), nth & 1u, abort_flag);
       tc_fence_after();
-      const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + (seg & 7u));
-      const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
       const bool whole = from_zero && c.j + 1 == c.nb;
       if (wide) ov = z == 0.f ? 0.f : ex2(ov - static_cast<float>(kTopQ));
       const int pr = tile * 128 + r;
@@ -863,10 +862,12 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
         part[32] = z;
       }
       // z = 0: a row without a key
-      const float inv = poison ? __uint_as_float(0x7fc00000u) : (z == 0.f ? 0.f : ov / z);
-      const float keep = poison ? inv : ov;
+      const float inv = z == 0.f ? 0.f : ov / z;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
+        const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + 4 * (seg & 7u) + cc);
+        const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
+        const float by = poison ? __uint_as_float(0x7fc00000u) : (whole ? inv : ov);
         uint32_t orr[32];
         KVQ_LD32(orr, o_col + 32u * cc);
         tmem_wait_ld();
@@ -874,7 +875,7 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
           uint32_t ob[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            ob[e] = pack_bf16(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+            ob[e] = pack_bf16(__uint_as_float(orr[2 * e]) * by, __uint_as_float(orr[2 * e + 1]) * by);
           if (real) {
             uint4* dst = reinterpret_cast<uint4*>(p.O + row * D + 32 * cc);
 #pragma unroll
@@ -883,7 +884,7 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(2 + 32 * cc + e) * 32] = __uint_as_float(orr[e]) * keep;
+          for (int e = 0; e < 32; ++e) part[(2 + 32 * cc + e) * 32] = __uint_as_float(orr[e]) * by;
         }
       }
       tc_fence_before();
@@ -922,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
   if (!p.plan.count && warp == 0) warp_prefix(p.t, p.RI, kBT, s_pre);
   if (threadIdx.x == 32) {
     *abort_flag = 0;
-    for (int i = 0; i < 8; ++i) s_bad[i] = 0;
+    for (int i = 0; i < 8 * 4; ++i) s_bad[i] = 0;
     for (uint32_t u = 0; u < nu; ++u) {
       mbar_init(bar(RING_FULL + 2 * u), 1);
       mbar_init(bar(RING_FULL + 2 * u + 1), 1);

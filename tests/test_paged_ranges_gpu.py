@@ -147,3 +147,38 @@ def test_empty_rows_and_two_sequences_of_other_sizes():
             err = np.abs(got[r0:r1] - want)
             assert (err <= 2.0 ** -8 * (size + np.abs(want)) + 2.0 ** -22 * size.max(-1, keepdims=True)).all(), (b, splits)
     K.check(DEV)
+
+
+@pytest.mark.parametrize("bits,D,n,dtype", SHAPES + [(4, 128, 3, torch.bfloat16), (8, 64, 2, torch.bfloat16)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("wide", [False, True])
+def test_value_scale_that_is_not_finite(bits, D, n, dtype, bad, wide):
+    """It is the scale of one token's 32 features: rows that see the token are not
+    finite there and as ever elsewhere, rows before it as ever."""
+    rng = np.random.default_rng(47)
+    s = Sequences(rng, [300], 1, D, bits, 32, 64)
+    raw = rng.standard_normal((2, 300, 1, D)).astype(np.float32)
+    if wide:
+        raw[1, :40] *= 2.0 ** 30
+    s.append([300], raw=raw)
+    q = bf16_values(rng.standard_normal((n, 4, D)).astype(np.float32))
+    at, hit = 300 - (n + 1) // 2, slice(32, min(D, 64))       # the token, its features
+
+    def run(splits):
+        return K.paged_attend(to_dev(q, dtype), s.cache, i32(s.table), i32([300]), i32([0, n]), n, D ** -0.5,
+                              splits=splits).float()
+
+    vs = s.cache.v_scales.view(s.cache.pages, 1, 64, -1)
+    page, row = int(s.table[0, at // 64]), at % 64
+    was = vs[page, 0, row, 1].clone()
+    for splits in (0, 1, 6):
+        want = run(splits)
+        vs[page, 0, row, 1] = bad
+        got = run(splits)
+        vs[page, 0, row, 1] = was
+        sees = n - (300 - at)                                 # the first row that does
+        assert torch.equal(got[:sees], want[:sees])
+        assert not torch.isfinite(got[sees:, :, hit]).any()
+        got[sees:, :, hit] = want[sees:, :, hit]
+        assert torch.equal(got, want)
+    K.check(DEV)
