@@ -21,7 +21,7 @@
 // instructions, 7 cycles at full issue; half of these take the codes apart (a
 // shift and one three-input logic operation make two bf16 integers of a
 // word's nibbles 16 bits apart).  Issue is 58 % busy, the integer pipe 48 %: 32
-// x 4096 keys of 8 KV heads (168 MB) take 54.5 us, 3.1 TB/s; at 8 bits, where a
+// x 4096 keys of 8 KV heads (168 MB) take 52.5 us, 3.2 TB/s; at 8 bits, where a
 // byte costs fewer instructions, 455 MB take 122 us, 3.7 TB/s, 56 % of the
 // measured copy rate.  Small calls (one sequence, 10.6 us) are two launches and the
 // latency of a few dependent loads each.  A 32-token block of one page -- codes and
@@ -370,7 +370,6 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
 
     // ---- q' = q ks of this group, split over the two columns of the row ----
     uint32_t bq[NT][C::SETS][D / 8];
-    float corr[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float4* sq = reinterpret_cast<const float4*>(s_q) + n * (C::FL / 4) * 16 + (g >> 1) * 4 + c;
@@ -420,20 +419,13 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
           }
         }
       }
-      // the codes' offset: the operand holds 16 + n (and 256 + 16 n), so each
-      // score is too large by that constant times the sum of q' (f32 rows take
-      // it from the operand instead: the larger sums would round away more)
-      corr[n] = 0.f;
-      if (NS == 2) {
-        float cc[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-        for (int k = 0; k < D / 8; k += 2) mma(cc, ones, bq[n][0][k], bq[n][0][k + 1]);
-        corr[n] = (BITS == 4 ? -23.f : -399.f) * (cc[0] + cc[1]);
-      }
     }
 
     // ---- scores of the block: lane = row c of each tile, tokens g + 8 i ------
+    // The codes' offset (the operand holds 16 + n, or 256 + 16 n) is taken from the
+    // operand: taken from the score instead, as that constant times the sum of q', it
+    // cost a score the precision of the largest q', though its code may be zero (a
+    // channel of zeros has the scale 1, one with an outlier the outlier's).
     // The tensor cores' sums are cut off, not rounded: f32 rows add them up
     // outside, rounded, a word's at a time, or the loss grows with D (and, below,
     // with the length).
@@ -485,12 +477,10 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
                               nibbles<1, false>(wb[k])};
             uint32_t a1[4] = {nibbles<2, false>(wa[k]), nibbles<2, false>(wb[k]), nibbles<3, false>(wa[k]),
                               nibbles<3, false>(wb[k])};
-            if (NS == 3) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                a0[e] = add_bf16x2(a0[e], 0xC1B8C1B8u);       // -23
-                a1[e] = add_bf16x2(a1[e], 0xC1B8C1B8u);
-              }
+            for (int e = 0; e < 4; ++e) {
+              a0[e] = add_bf16x2(a0[e], 0xC1B8C1B8u);         // -23
+              a1[e] = add_bf16x2(a1[e], 0xC1B8C1B8u);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) products(acc[n], a0, a1, bq[n], 4 * x, 4 * x + 2);
@@ -499,12 +489,10 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
                               nibbles<2, false>(wb[k])};
             uint32_t a1[4] = {nibbles<1, true>(wa[k]), nibbles<1, true>(wb[k]), nibbles<3, true>(wa[k]),
                               nibbles<3, true>(wb[k])};
-            if (NS == 3) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                a0[e] = add_bf16x2(a0[e], 0xC1F8C1F8u);       // -31
-                a1[e] = add_bf16x2(a1[e], 0xC3B8C3B8u);       // -368
-              }
+            for (int e = 0; e < 4; ++e) {
+              a0[e] = add_bf16x2(a0[e], 0xC1F8C1F8u);         // -31
+              a1[e] = add_bf16x2(a1[e], 0xC3B8C3B8u);         // -368
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) products(acc[n], a0, a1, bq[n], 2 * x, 2 * x);
@@ -513,8 +501,8 @@ __global__ void __launch_bounds__(32 * Cfg<BITS, D, NT, NS>::kWarps, Cfg<BITS, D
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        sc[n][2 * hh] = acc[n][0] + acc[n][1] + corr[n];
-        sc[n][2 * hh + 1] = acc[n][2] + acc[n][3] + corr[n];
+        sc[n][2 * hh] = acc[n][0] + acc[n][1];
+        sc[n][2 * hh + 1] = acc[n][2] + acc[n][3];
       }
     }
 

@@ -62,9 +62,11 @@ def check(s, q, G, dtype, splits=0, scale=None, b=0):
                           f"{err[bad][0]:.3e} > {tol[bad][0]:.3e}"
 
 
-# rows of four heads a KV head
-SHAPES = [(4, 128, 100, torch.bfloat16), (8, 128, 100, torch.bfloat16),
-          (4, 64, 100, torch.bfloat16), (8, 64, 24, torch.bfloat16), (8, 64, 100, torch.float32),
+# rows of four heads a KV head: the kernels of few and of many
+SHAPES = [(4, 128, 1, torch.bfloat16), (8, 64, 2, torch.bfloat16), (4, 128, 100, torch.bfloat16),
+          (8, 128, 100, torch.bfloat16),
+          (8, 128, 1, torch.bfloat16), (4, 64, 100, torch.bfloat16), (8, 64, 24, torch.bfloat16),
+          (8, 64, 100, torch.float32),
           (4, 80, 9, torch.bfloat16), (8, 80, 5, torch.float32)]
 
 
@@ -149,7 +151,7 @@ def test_empty_rows_and_two_sequences_of_other_sizes():
     K.check(DEV)
 
 
-@pytest.mark.parametrize("bits,D,n,dtype", SHAPES + [(4, 128, 3, torch.bfloat16), (8, 64, 2, torch.bfloat16)])
+@pytest.mark.parametrize("bits,D,n,dtype", SHAPES + [(4, 128, 3, torch.bfloat16)])
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 @pytest.mark.parametrize("wide", [False, True])
 def test_value_scale_that_is_not_finite(bits, D, n, dtype, bad, wide):
