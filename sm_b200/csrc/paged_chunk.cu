@@ -794,10 +794,14 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
         }
       }
       // p = exp2(s * qs - m_ref + kTopP) as fp16 over the columns already read,
-      // 16 at a time, the next ones on their way
+      // 16 at a time, the next ones on their way.  (m_ref is a product's rounding and
+      // the fused product is not rounded: the largest p is off by half an ulp of
+      // m_ref in its exponent, the same for all of a row's.  That is 1/8 below 2^22;
+      // beyond, the other body rounds the products too, or p could leave fp16.)
       const float m_top = kTopP - m_ref;
       u64 z2 = 0ull;
-      if (plain) {
+      const bool far = __any_sync(0xffffffffu, fabsf(m_ref) > 4194304.f);
+      if (plain && !far) {
         uint32_t s0[16], s1[16];
         const u64 f2 = pack2(qs, qs), c2 = pack2(m_top, m_top);
         auto columns = [&](const uint32_t (&sr)[16], int cc) {
@@ -832,8 +836,11 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float p0 = e < left ? ex2(fmaf(__uint_as_float(sr[e]), qs, m_top)) : 0.f;
-              const float p1 = e + 1 < left ? ex2(fmaf(__uint_as_float(sr[e + 1]), qs, m_top)) : 0.f;
+              const float y0 = __uint_as_float(sr[e]), y1 = __uint_as_float(sr[e + 1]);
+              const float x0 = far ? __fmul_rn(y0, qs) - m_ref + kTopP : fmaf(y0, qs, m_top);
+              const float x1 = far ? __fmul_rn(y1, qs) - m_ref + kTopP : fmaf(y1, qs, m_top);
+              const float p0 = e < left ? ex2(x0) : 0.f;
+              const float p1 = e + 1 < left ? ex2(x1) : 0.f;
               z2 = add2(z2, pack2(p0, p1));
               pk[e >> 1] = pack_f16(p0, p1);
             }

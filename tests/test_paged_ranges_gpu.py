@@ -64,9 +64,8 @@ def check(s, q, G, dtype, splits=0, scale=None, b=0):
 
 # rows of four heads a KV head: the kernels of few and of many
 SHAPES = [(4, 128, 1, torch.bfloat16), (8, 64, 2, torch.bfloat16), (4, 128, 100, torch.bfloat16),
-          (8, 128, 100, torch.bfloat16),
-          (8, 128, 1, torch.bfloat16), (4, 64, 100, torch.bfloat16), (8, 64, 24, torch.bfloat16),
-          (8, 64, 100, torch.float32),
+          (8, 128, 100, torch.bfloat16), (8, 128, 1, torch.bfloat16), (4, 64, 100, torch.bfloat16),
+          (8, 64, 24, torch.bfloat16), (8, 64, 100, torch.float32),
           (4, 80, 9, torch.bfloat16), (8, 80, 5, torch.float32)]
 
 
@@ -184,3 +183,25 @@ def test_value_scale_that_is_not_finite(bits, D, n, dtype, bad, wide):
         got[sees:, :, hit] = want[sees:, :, hit]
         assert torch.equal(got, want)
     K.check(DEV)
+
+
+@pytest.mark.parametrize("bits,D,n,dtype", SHAPES)
+@pytest.mark.parametrize("size", [2.0 ** k for k in (8, 12, 14, 16, 18, 20, 30, 60)])
+def test_scores_of_any_size(bits, D, n, dtype, size):
+    """Scores up to 2^69: keys of whole numbers in groups of scale 1 and queries
+    of powers of two, so that equal scores are equal in any precision and others
+    far apart.  A row is the mean of its best keys' values."""
+    rng = np.random.default_rng(46)
+    top = 7 if bits == 4 else 127
+    s = Sequences(rng, [200], 1, D, bits, 32, 32)
+    raw = np.zeros((2, 200, 1, D), np.float32)
+    raw[0, :, 0, 0] = rng.integers(-top + 1, top, 200)
+    raw[0, 5::32, 0, 0] = -top                           # in every group, and no key but one at the other end
+    raw[0, 77, 0, 0] = top
+    raw[0, :, 0, 1] = top                                # the same for all keys
+    raw[1] = rng.standard_normal((200, 1, D))
+    s.append([200], raw=raw)
+    q = np.zeros((n, 4, D), np.float32)
+    q[..., 0] = size * rng.choice([-1.0, 1.0], (n, 4))
+    q[..., 1] = size * rng.choice([-1.0, 1.0], (n, 4))
+    check(s, q, 4, dtype, scale=1.0)
