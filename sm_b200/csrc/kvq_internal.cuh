@@ -52,13 +52,14 @@ bool make_geometry(const kvq_cache* c, Geometry* g);
 // with griddep_wait() -- which returns once every earlier grid on the stream
 // has completed and its memory is visible -- before any global-memory
 // access; it then lets the next kernel be scheduled.  Without a predecessor
-// (or without the launch attribute) both are no-ops.  Two kernels always run
-// right after one of the library's own, which has waited for every grid
-// before it by the time it lets them be scheduled, and read some of the
-// call's inputs (which no kernel of the library writes) before their own
-// wait, through the L2 (ld.global.cg): the split merge computes its plan
-// from the lengths, and the window kernel (griddep_release / griddep_join
-// below) does all its work.
+// (or without the launch attribute) both are no-ops.  Some kernels always run
+// right after one of the same call's, which has waited for every grid before
+// the call by the time it lets them be scheduled, and read some of the call's
+// inputs before their own wait, through the L2 (ld.global.cg): the split
+// merges compute their plan from the lengths (and, paged, the row offsets), and
+// the window kernel and the paged chunk kernel's preparation (griddep_release /
+// griddep_join below) do all their work.  What they read the call itself does
+// not write, whatever wrote it before.
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

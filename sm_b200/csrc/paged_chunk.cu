@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
     paged_prepare_kernel(Batch t, const float* k_scales, const float* v_scales, uint32_t* tops, int parts,
                          const uint4* Q, uint4* Qh, float* q_pow, long long rows, int beside, unsigned int* err) {
   // beside: the kernel before is the plan's, which has waited for every other
-  // and writes what this one does not touch
+  // and writes what this one does not touch.  (All that is read may just have been
+  // written by such a grid, of the library too: through the L2.)
   if (beside) griddep_release();
   else griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
     for (int i = 0; i < kRowsPerLane; ++i) {
       const long long row = first + i * PASS;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < rows) x[i] = __ldg(Q + row * L + l);
+      if (row < rows) x[i] = __ldcg(Q + row * L + l);
     }
 #pragma unroll
     for (int i = 0; i < kRowsPerLane; ++i) {
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
     long long own = 0;
     if (g < groups) {
       const int pi = 32 * g / t.P;
-      own = (static_cast<long long>(read_page(__ldg(table + pi), t.pages, err)) * t.H + h) * t.P + 32 * g - pi * t.P;
+      own = (static_cast<long long>(read_page(__ldcg(table + pi), t.pages, err)) * t.H + h) * t.P + 32 * g - pi * t.P;
     }
     const int n = min(32, (groups - g0 + stride - 1) / stride);
     for (int i0 = 0; i0 < n; i0 += 4) {
@@ -535,8 +536,8 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {                       // (past the last one: the last one again)
         const long long tok = __shfl_sync(0xffffffffu, own, min(i0 + i, n - 1));
-        x[i][0] = __ldg(reinterpret_cast<const Vec*>(k_scales + (tok >> 5) * D) + lane);
-        x[i][1] = __ldg(reinterpret_cast<const Vec*>(v_scales + tok * (D / 32)) + lane);
+        x[i][0] = __ldcg(reinterpret_cast<const Vec*>(k_scales + (tok >> 5) * D) + lane);
+        x[i][1] = __ldcg(reinterpret_cast<const Vec*>(v_scales + tok * (D / 32)) + lane);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
