@@ -421,7 +421,8 @@ KVQ_API kvq_status kvq_paged_attend(const void* Q, kvq_dtype q_dtype, const kvq_
 KVQ_API size_t kvq_paged_workspace_size(const kvq_paged_cache* cache, kvq_dtype q_dtype, int32_t S, int32_t T,
                                         int32_t max_q, int32_t H_q, int32_t splits);
 
-/* Name of the attention kernel kvq_paged_attend would run, for logs and tests. */
+/* Name of the attention kernel kvq_paged_attend would run, for logs and tests.
+ * max_q: the smaller of the call's max_q and T (the call itself takes that). */
 KVQ_API const char* kvq_paged_kernel_name(const kvq_paged_cache* cache, kvq_dtype q_dtype, int32_t max_q,
                                           int32_t H_q);
 

@@ -531,9 +531,11 @@ def paged_workspace_size(cache: PagedCache, dtype: torch.dtype, S: int, T: int, 
                                             H_q, splits))
 
 
-def paged_kernel_name(cache: PagedCache, dtype: torch.dtype, max_q: int, H_q: int) -> str:
-    return lib.kvq_paged_kernel_name(cache._ref, KVQ_F32 if dtype == torch.float32 else KVQ_BF16, int(max_q),
-                                     int(H_q)).decode()
+def paged_kernel_name(cache: PagedCache, dtype: torch.dtype, max_q: int, H_q: int, T: int | None = None) -> str:
+    """The kernel paged_attend runs for these sizes.  ``T``: the call's rows; without it max_q is taken to be no
+    larger bound than they are."""
+    return lib.kvq_paged_kernel_name(cache._ref, KVQ_F32 if dtype == torch.float32 else KVQ_BF16,
+                                     int(max_q if T is None else min(max_q, T)), int(H_q)).decode()
 
 
 def paged_attend(Q: torch.Tensor, cache: PagedCache, block_table: torch.Tensor, lengths: torch.Tensor,
