@@ -5,8 +5,8 @@ It only marshals arguments: torch tensors supply device pointers, the current
 CUDA stream and device memory; every step of quantize/pack and attention runs
 in the library's kernels.  The paged calls marshal theirs in a small extension
 (``_calls.so``, ``csrc/torch_calls.cpp``), since a serving loop makes them once
-a layer.  If ``libkvq.so`` or ``_calls.so`` is missing the import fails: there
-is no fallback of any kind.
+a layer.  If ``libkvq.so`` is missing the import fails, if ``_calls.so`` is the
+paged calls do: there is no fallback of any kind.
 
     cache = sm_b200.PackedCache(B, H_kv, N_cap, D, bits=4, group=32)
     sm_b200.pack(K, V, cache)                     # K, V [B, H_kv, T, D] fp32/bf16
@@ -142,10 +142,21 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+
+class _NoCalls:
+    """In place of the extension where it does not load: every call raises."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_calls.so not built for this torch: run `python sm_b200/build.py` ({self._why})")
+
+
 try:
     from . import _calls               # the paged calls: argument checks and tensors in C++
 except ImportError as e:
-    raise ImportError(f"_calls.so not built: run `python sm_b200/build.py` ({e})") from e
+    _calls = _NoCalls(e)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
