@@ -27,6 +27,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libkvq.so")
 CALLS = os.path.join(HERE, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_STAMP = os.path.join(BUILD, "calls.stamp")         # what _calls.so was built against
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
@@ -68,9 +69,28 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def build_calls(force: bool = False) -> str:
+def _calls_against() -> str:
+    import torch
+    return f"torch {torch.__version__} at {os.path.dirname(torch.__file__)}, python {sys.version_info[:2]}"
+
+
+def stamp_calls() -> None:
+    os.makedirs(os.path.dirname(CALLS_STAMP), exist_ok=True)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_calls_against())
+
+
+def calls_up_to_date() -> bool:
     deps = [CALLS_SRC, os.path.abspath(__file__), *glob.glob(os.path.join(ROOT, "include", "*.h"))]
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+    if not (os.path.exists(CALLS) and os.path.exists(CALLS_STAMP)):
+        return False
+    with open(CALLS_STAMP) as f:
+        same = f.read() == _calls_against()
+    return same and all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps)
+
+
+def build_calls(force: bool = False) -> str:
+    if not force and calls_up_to_date():
         return CALLS
     import sysconfig
     import torch
@@ -87,6 +107,7 @@ def build_calls(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {CALLS_SRC}:\n{res.stderr}")
     os.replace(tmp, CALLS)
+    stamp_calls()
     return CALLS
 
 

@@ -1,13 +1,24 @@
-"""CPU test of the package without the binding's extension."""
+"""CPU tests of the package without the binding's extension, and of what its
+build holds to be up to date."""
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 
+import torch
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def build_module():
+    spec = importlib.util.spec_from_file_location("_kvq_build_test", os.path.join(ROOT, "sm_b200", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
 
 
 def test_contiguous_calls_need_no_extension(tmp_path):
@@ -35,3 +46,24 @@ print("fine")
     r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
                        env={**os.environ, "PYTHONPATH": str(tmp_path)})
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr
+
+
+def test_extension_of_another_torch_is_stale(tmp_path, monkeypatch):
+    """File times do not tell: a torch installed anew brings other libraries."""
+    b = build_module()
+    so = tmp_path / "_calls.so"
+    monkeypatch.setattr(b, "CALLS", str(so))
+    monkeypatch.setattr(b, "CALLS_STAMP", str(tmp_path / "calls.stamp"))
+    assert not b.calls_up_to_date()
+    so.write_bytes(b"")
+    assert not b.calls_up_to_date()                  # built by something that left no stamp
+    b.stamp_calls()
+    assert b.calls_up_to_date()
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert not b.calls_up_to_date()
+    monkeypatch.undo()
+    monkeypatch.setattr(b, "CALLS", str(so))
+    monkeypatch.setattr(b, "CALLS_STAMP", str(tmp_path / "calls.stamp"))
+    assert b.calls_up_to_date()
+    os.utime(so, (0, 0))
+    assert not b.calls_up_to_date()
