@@ -1223,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(const __grid_c
         uint32_t x[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const uint32_t* at = tops + min(i + e, n - 1) * (4 * kParts) + lane;
+          const uint32_t* at = tops + static_cast<long long>(min(i + e, n - 1)) * (4 * kParts) + lane;
           x[e] = __ldcg(at);
           y[e] = __ldcg(at + 2 * kParts);
         }
