@@ -314,7 +314,11 @@ KVQ_API kvq_status kvq_selftest_timeout(const void* Q, kvq_dtype q_dtype, const 
  * the pages: k_tail, device float32 [tail_slots, H_kv, g, D], 16-byte
  * aligned; row r of a slot is the (rotated) key of token g * (len / g) + r of
  * the sequence that owns the slot, for r < len % g.  kvq_paged_append reads
- * and keeps it; a sequence that moves to another slot takes its rows along.
+ * and keeps it; a sequence that moves to another slot takes its rows along.  A
+ * sequence may be cut back (drafts that were rejected) to any length from
+ * g * (len / g) on; to go back over a group's end, the caller copies the slot
+ * before those tokens are appended, puts it back, and appends again what it
+ * keeps of them.
  *
  * Batches are ragged: the rows of sequence b's new tokens are rows
  * [cu[b], cu[b + 1]) of the call's row tensors (cu: device int32 [S + 1],
