@@ -65,7 +65,7 @@ typedef enum {
   KVQ_ERR_DEVICE = 6,       /* a kernel recorded an internal inconsistency */
   KVQ_ERR_TIMEOUT = 7,      /* a bounded wait inside a kernel ran out */
   KVQ_ERR_UNSUPPORTED = 8,  /* valid arguments outside what this library implements */
-  KVQ_ERR_INDEX = 9         /* a page number or a position outside its range (device-detected) */
+  KVQ_ERR_INDEX = 9         /* a page number, a tail slot or a position outside its range (device-detected) */
 } kvq_status;
 
 typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1 } kvq_dtype;
@@ -327,6 +327,10 @@ KVQ_API kvq_status kvq_selftest_timeout(const void* Q, kvq_dtype q_dtype, const 
  * of the rows a sequence has in this call, known on the host; lengths count
  * the new tokens.
  *
+ * Limits of all three calls: KVQ_ERR_UNSUPPORTED for more than 8192 sequences or
+ * 65535 KV heads and for D > 256; KVQ_ERR_ARG where max_pages * P passes
+ * 2^31 - 256.
+ *
  * Device-detected errors (kvq_check): KVQ_ERR_LENGTH for a sequence with rows
  * whose length is below its row count or beyond max_pages * P, or for a cu
  * that is not as stated (rows are then clamped to [0, T) and max_new);
@@ -366,7 +370,7 @@ typedef struct {
  * over calls.  Sequences of one call must own different slots and pages.
  * Errors: KVQ_ERR_ARG, KVQ_ERR_ALIGN (K, V, int32 arrays not aligned to their
  * element size; cache arrays, k_tail not to 16 bytes), KVQ_ERR_UNSUPPORTED
- * (D > 256, or g * D > 32768), KVQ_ERR_CUDA.
+ * (the limits above, or g * D > 32768), KVQ_ERR_CUDA.
  */
 KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* cache, const void* K, int64_t k_stride,
                                     const void* V, int64_t v_stride, kvq_dtype in_dtype,
@@ -383,7 +387,8 @@ KVQ_API kvq_status kvq_paged_append(const kvq_paged_cache* cache, const void* K,
  * checking a cache, or kernels that want dense keys.  The tokens must have
  * been appended; a token past max_pages * P gives a zero row and
  * KVQ_ERR_LENGTH.
- * Errors: KVQ_ERR_ARG, KVQ_ERR_ALIGN, KVQ_ERR_CUDA.
+ * Errors: KVQ_ERR_ARG, KVQ_ERR_ALIGN, KVQ_ERR_UNSUPPORTED (the limits above),
+ * KVQ_ERR_CUDA.
  */
 KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t* block_table,
                                     int32_t max_pages, const int32_t* starts, const int32_t* cu_rows,
