@@ -17,12 +17,14 @@
 // vector form (features in eights, groups a power of two) gives K and V a CTA
 // each, eight features a lane; a call of one token a sequence has V in K's.
 //
-// Bound by memory where the call is large, by latency where it is small.  8
-// thousand new tokens of 8 heads, D = 128, and reading 8 thousand back: 140 MB in
-// 63 us (2.2 TB/s); one token of each of 64 sequences, and
-// as many read back: 15.5 us, of which two launches and their dependent loads (cu,
-// lengths, pages, rows) are nearly all.  In the scalar form these take 130 and 26
-// us; it serves the other shapes.
+// Bound by latency and issue.  8 thousand new tokens of 8 heads, D = 128, and
+// reading 8 thousand back: 140 MB in 63.5 us (2.2 TB/s), captured alone 44 us the
+// append (issue 47 %) and 24 the read-back (52 %).  One token of each of 64
+// sequences, and their groups read back: 14.8 us, of which two launches are 10
+// (groups of 8 of 9 sequences take that); captured cold, the append's 512 CTAs wait
+// for instructions more than for loads (12.4 us; the read-back 9.1).  In the scalar
+// form the two take 130 and 26 us; it serves the other shapes, groups of 64 among
+// them (8 thousand tokens with the read-back: 184 us).
 #include "f32x2.cuh"
 #include "paged.cuh"
 #include "quant.cuh"
@@ -228,9 +230,9 @@ __device__ __forceinline__ void append_group(const AppendParams& p, float* s_x, 
 // registers, twice the loads in flight.  A K CTA holds the group's rows in
 // registers, PASS rows a thread; a channel's maximum goes over the thread's
 // rows, the warp's and (through shared memory) the four warps'.  Arithmetic is
-// on pairs (f32x2).  Needs D and the pairs' distance in whole vectors, groups
-// of 8 to 64 whose features divide D, and aligned rows; append_group above
-// takes the rest.
+// on pairs (f32x2).  Needs D and the pairs' distance in whole vectors, aligned rows,
+// and groups of 8 or 32, or of 16 where D is at most 128, that divide D (what
+// pick_append has an instance for); append_group above takes the rest.
 constexpr float kRound = 12582912.f;               // 1.5 * 2^23: x + kRound has rint(x) in its low bits
 
 // Eight floats as four pairs.
@@ -761,7 +763,8 @@ void fill_geometry(const Geometry& g, int max_pages, P* p) {
   p->v_scales_head = static_cast<long long>(g.v_scales_head);
 }
 
-// Whether the vector form's conditions hold (figures of both forms at the top).
+// Whether the vector form's conditions hold but for the group's size, which
+// pick_append knows (figures of both forms at the top).
 bool vector_form(const AppendCall& a) {
   const int D = a.g.D, g = a.g.group;
   const size_t es = a.in_dtype == KVQ_BF16 ? 2 : 4;

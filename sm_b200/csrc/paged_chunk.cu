@@ -19,13 +19,13 @@
 //
 // What bounds it: at 128 rows a block costs 4 * 128 * D * 128 FLOPs for 160
 // (288) bytes a key at D = 128, so the tensor pipe and not memory; 4 x 64 rows
-// of 4 heads over 16384 keys take 107 us, 640 TFLOP/s, 40 % of the measured bf16
+// of 4 heads over 16384 keys take 108 us, 635 TFLOP/s, 40 % of the measured bf16
 // rate.  The MMAs alone would take 2.6k cycles a block of two tiles.  A block
 // takes about 4.9k: V is decoded (2.0 to 2.5k), then P V of the first tile, Q K of
 // its next block and P V of the second run before V's tile is free again, while
 // the two softmaxes (3k each) and K's decode run beside that chain.  So two row
 // tiles are in flight, and a lone tile has its scores twice: the next block's are
-// there before this one's values (24 x 40 rows: 133 -> 119 us).
+// there before this one's values (24 x 40 rows: 133 -> 119 us at the time, 120 now).
 //
 // The kernel's size counts as well: roles that run side by side share the
 // instruction cache, and at 130 KB of code instead of 70 everything took a
@@ -47,7 +47,7 @@
 // Warp roles (20 warps, 96 registers each):
 //   0        producer: two lanes copy 32 keys each (codes and scales) of half a
 //            K or V block into a ring; order K(0), K(1), V(0), K(2), ...
-//   1        MMA issuer (one thread) and TMEM owner
+//   1        MMA issuer (the warp runs converged, one lane issues) and TMEM owner
 //   2        Q loader; leaves a segment's powers to the others
 //   3        finds the CTA's form, which says what bodies 4..19 run
 //   4..7     softmax of tile 0 (a thread a row), 8..11 of tile 1
@@ -79,7 +79,7 @@ constexpr int kThreads = 640;
 constexpr int kDecodeWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;
-constexpr int kTileHalf = kBT * 128;              // 16 KB: 128 rows x 64 bf16
+constexpr int kTileHalf = kBT * 128;              // 16 KB: 128 rows x 64 fp16
 constexpr int kMaxUnits = 12;                    // half-units of the ring
 
 // Powers of two that keep the fp16 tiles in range.  A query row is multiplied by
@@ -101,7 +101,8 @@ constexpr int kMaxUnits = 12;                    // half-units of the ring
 //           So a key that a row does not see changes nothing of the row's, a group
 //           of zeros (whose scale is 1) is a group of zeros, and what is lost is
 //           what float32 sums lose too: contributions below 2^-21 of the largest.
-//           Its softmax waits for V's tile: more time, for data that is rarely met.
+//           Its softmax waits for V's tile and takes S apart three times: 24 x 40
+//           rows 126 -> 395 us, prompts 387 -> 560, for data that is rarely met.
 constexpr int kTop = 7, kTopQ = 14;
 constexpr float kTopP = 7.f;                     // p <= 2^(kTopP + kLazy) = 2^15
 constexpr int kExpMin = -100, kExpMax = 127;

@@ -17,13 +17,13 @@
 // of their norm off instead of 4e-7, for 0.7 us of 16 at the time).
 //
 // What bounds it: at four rows a KV head a 4-bit token costs 160 bytes, 7
-// cycles of one SM's share of the measured memory bandwidth, and about 28 warp
+// cycles of one SM's share of the measured memory bandwidth, and about 27 warp
 // instructions, 7 cycles at full issue; half of these take the codes apart (a
 // shift and one three-input logic operation make two bf16 integers of a
-// word's nibbles 16 bits apart).  Issue is 58 % busy, the integer pipe 48 %: 32
+// word's nibbles 16 bits apart).  Issue is 59 % busy, the integer pipe 53 %: 32
 // x 4096 keys of 8 KV heads (168 MB) take 52.5 us, 3.2 TB/s; at 8 bits, where a
 // byte costs fewer instructions, 455 MB take 122 us, 3.7 TB/s, 56 % of the
-// measured copy rate.  Small calls (one sequence, 10.6 us) are two launches and the
+// measured copy rate.  Small calls (one sequence, 10.5 us) are two launches and the
 // latency of a few dependent loads each.  A 32-token block of one page -- codes and
 // scales -- is fetched by the warp that uses it with 16-byte asynchronous
 // copies (two blocks in flight a warp), placed so that every later
@@ -719,7 +719,7 @@ struct Run {
     p.O = a.O;
     p.partials = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan_bytes(a, C::RI));
     // no more CTAs than a fourth of the blocks that the tables could hold (one
-    // sequence of 1000 keys, 8 heads: 10.8 us with 296 CTAs, 9.9 with 64)
+    // sequence of 1000 keys, 8 heads: 11.1 us with 296 CTAs, 10.6 with 64)
     const long long most = plan_items(a, C::RI) * a.g.H_kv * ((static_cast<long long>(p.t.cap) + kBT - 1) / kBT);
     const int n = a.splits > 0 ? a.splits : static_cast<int>(std::min<long long>(ctas(a), (most + 3) / 4));
     p.workers = n * C::kWarps;
