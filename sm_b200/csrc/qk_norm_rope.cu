@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(kThreads) qk_vec_kernel(Params p) {
 }
 
 // Any width, alignment and rotation: a warp per row, the row in shared memory
-// (so a row may be written where it was read).
+// (so a row may be written where it was read).  An element a lane and load: 8
+// thousand tokens of 32 + 8 heads at D = 80 or 96 take 159 us.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) qk_any_kernel(Params p) {
   griddep_wait();
