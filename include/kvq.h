@@ -410,13 +410,13 @@ KVQ_API kvq_status kvq_paged_gather(const kvq_paged_cache* cache, const int32_t*
  * and the weighted values are float32; O is rounded once.  What lies behind a
  * row's position may hold anything, infinities and NaN included.  A V scale that
  * is not finite makes a row that sees its token not finite in that scale's g
- * features; a K scale that is not finite makes the whole row so, unless its
- * scores are all minus infinity.
+ * features; a K scale that is not finite may make the whole row so.
  * Calls of many bf16 rows (kvq_paged_kernel_name says "paged_chunk_tcgen05")
  * round K, V and the softmax's weights once to fp16, in ranges that keep eleven
  * bits of each: a key's values lose precision only where they are 2^28 times
  * smaller than its largest, weights times values where they are 2^21 times
- * smaller than the row's largest.
+ * smaller than the row's largest.  Calls of few bf16 rows hold a query's products
+ * with K's scales, and the weights' with V's, in sixteen bits.
  * Errors: as kvq_attend; KVQ_ERR_UNSUPPORTED also for T * H_q >= 2^30.
  */
 KVQ_API kvq_status kvq_paged_attend(const void* Q, kvq_dtype q_dtype, const kvq_paged_cache* cache,

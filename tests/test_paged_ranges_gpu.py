@@ -205,3 +205,26 @@ def test_scores_of_any_size(bits, D, n, dtype, size):
     q[..., 0] = size * rng.choice([-1.0, 1.0], (n, 4))
     q[..., 1] = size * rng.choice([-1.0, 1.0], (n, 4))
     check(s, q, 4, dtype, scale=1.0)
+
+
+@pytest.mark.parametrize("bits,D,n,dtype", SHAPES)
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 2.0 ** 100])
+@pytest.mark.parametrize("splits", [0, 1, 10])
+def test_key_scale_behind_a_row(bits, D, n, dtype, bad, splits):
+    """A key channel's scale in the last group, whatever it is: rows before the
+    group are as ever."""
+    rng = np.random.default_rng(48)
+    s = Sequences(rng, [300], 1, D, bits, 32, 32)
+    s.append([300])
+    q = bf16_values(rng.standard_normal((n, 4, D)).astype(np.float32))
+    s.cache.k_scales.view(s.cache.pages, 1, 1, D)[int(s.table[0, 288 // 32]), 0, 0, 5] = bad
+    got = K.paged_attend(to_dev(q, dtype), s.cache, i32(s.table), i32([300]), i32([0, n]), n, D ** -0.5,
+                         splits=splits).double().cpu().numpy()
+    K.check(DEV)
+    kd, vd = s.decoded(0)
+    before = max(0, n - 12)                                   # rows at positions below 288
+    want, size = rows64(q[:before], kd, vd, D ** -0.5, 300 - n)
+    err = np.abs(got[:before] - want)
+    assert (err <= 2.0 ** -8 * (size + np.abs(want)) + 2.0 ** -22 * size.max(-1, keepdims=True, initial=0)).all()
+    if np.isnan(bad):
+        assert np.isnan(got[before:]).all()
