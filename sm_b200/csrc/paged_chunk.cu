@@ -662,7 +662,8 @@ __device__ __forceinline__ void decode_role(const Cta<BITS, D>& cta) {
       if (start) ++seg;
       const unsigned long long key = static_cast<unsigned long long>(seg) << 32;
       if (kWideToo && ev == kWide)
-        decode_unit<BITS, D, true, true>(u, sm + M::kV, wk, lane, min(kBT, nv), 0.f, t0, key, s_bad + 4 * (seg & 7u), s_val);
+        decode_unit<BITS, D, true, true>(u, sm + M::kV, wk, lane, min(kBT, nv), 0.f, t0, key,
+                                         s_bad + 4 * (seg & 7u), s_val);
       else
         decode_unit<BITS, D, true, false>(u, sm + M::kV, wk, lane, min(kBT, nv), exp2i(kTop - ev), t0, key,
                                           s_bad + 4 * (seg & 7u), nullptr);
@@ -872,11 +873,15 @@ __device__ __forceinline__ void softmax_role(const Cta<BITS, D>& cta) {
       }
       // z = 0: a row without a key
       const float inv = z == 0.f ? 0.f : ov / z;
-#pragma unroll 1
+      uint32_t bad_mask = 0u;                           // feature groups with a non-finite scale that the row sees
+#pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         const unsigned long long bad = *reinterpret_cast<volatile unsigned long long*>(s_bad + 4 * (seg & 7u) + cc);
-        const bool poison = (bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim;
-        const float by = poison ? __uint_as_float(0x7fc00000u) : (whole ? inv : ov);
+        if ((bad >> 32) == seg && 0x7fffffff - static_cast<int>(bad & 0xffffffffu) < lim) bad_mask |= 1u << cc;
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        const float by = (bad_mask >> cc & 1u) ? __uint_as_float(0x7fc00000u) : (whole ? inv : ov);
         uint32_t orr[32];
         KVQ_LD32(orr, o_col + 32u * cc);
         tmem_wait_ld();
